@@ -142,15 +142,20 @@ def _spread(s, g, K):
     return s.repeat_interleave(g, -1)[..., :K]
 
 
+def _over(x, n):
+    """x / n, divided: a Python number as divisor would become a product with 1 / n."""
+    return x / torch.full((), n, dtype=x.dtype, device=x.device)
+
+
 def _quantize(W, g, with_zeros):
     """codes [E, N, K] (whole numbers as floats), scale and zero [E, N, groups], row_scale [E, N]"""
     K = W.shape[-1]
     if with_zeros:
         lo = _groups(W, g, torch.amin, 0.0).clamp(max=0)
-        t = (_groups(W, g, torch.amax, 0.0).clamp(min=0) - lo) / 15
+        t = _over(_groups(W, g, torch.amax, 0.0).clamp(min=0) - lo, 15)
     else:
-        t = _groups(W.abs(), g, torch.amax, 0.0) / 7
-    row = t.amax(-1) / 448
+        t = _over(_groups(W.abs(), g, torch.amax, 0.0), 7)
+    row = _over(t.amax(-1), 448)
     scale = torch.where(row[..., None] > 0, t / row[..., None], 0.0).float()
     scale = scale.to(torch.float8_e4m3fn).to(W.dtype)
     step = scale * row[..., None]
