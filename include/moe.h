@@ -396,6 +396,90 @@ moe_status_t moe_layer_forward_train(const moe_desc_t* desc, const void* x, cons
                                      size_t ws_bytes, void* bwd_ws, size_t bwd_ws_bytes,
                                      moe_stream_t stream);
 
+/* Gradients of the dispatch and of the merge, for layers whose experts are the caller's own: with
+ * moe_route, moe_permute and moe_combine they are the steps around any expert network (Tiny MoE
+ * sections 5, 6 and 9; "Top-k 路由" section "門控網路的梯度流").  The selection is fixed.
+ *
+ * moe_combine_backward: out[t] = sum_j gates[t,j] * y[inv[t,j]] gives
+ *     dy[inv[t,j]] = gates[t,j] * dout[t],   dgates[t,j] = <dout[t], y[inv[t,j]]>,
+ *   dgates = 0 where inv = -1.  A shared expert's gradient is dout itself.
+ *   dout [T, D], y and dy [A, D] (dtype); inv, gates and dgates as moe_combine's (K = k, or E
+ *   under expert choice; dgates fp32, every entry written).  Rows of dy that no assignment names
+ *   are not written.  dy or dgates may be NULL (not both): that gradient is left out, and y may
+ *   be NULL without dgates.  dy may be y itself; no other buffers may overlap.
+ * moe_permute_backward: x_perm[inv[t,j]] = x[t] gives
+ *     dx[t] = add[t] + sum_j dx_perm[inv[t,j]]   over j with inv[t,j] >= 0, in slot order.
+ *   dx_perm [A, D], dx [T, D] (dtype), every row of dx written; add [T, D] (dtype) or NULL: the
+ *   gradient that reaches x by other ways (router, shared experts, residual).  dx may be add
+ *   itself.
+ * Sums are fp32 in a fixed order (no atomics), rounded once; inv must name rows below A, each at
+ * most once, as moe_permute leaves it.  T = 0 returns MOE_OK without a launch. */
+moe_status_t moe_combine_backward(const moe_desc_t* desc, const void* dout, const void* y,
+                                  const int32_t* inv, const float* gates, void* dy,
+                                  float* dgates, moe_stream_t stream);
+moe_status_t moe_permute_backward(const moe_desc_t* desc, const void* dx_perm,
+                                  const int32_t* inv, const void* add, void* dx,
+                                  moe_stream_t stream);
+
+/* Expert weights in 4 bits with group scales ("别只比较 Top-k" expert-work account: a small decode
+ * batch streams the weights of the experts it touches, so their bytes are its time; the pages
+ * name no format, this one is the library's).  G stacked matrices [N, K] in the nn.Linear layout,
+ * K contracted, N and K multiples of 64, stand for
+ *     W[n, k] = row_scale[n] * scale[k / group, n] * (code[n, k] - zero[k / group, n])
+ *   codes     [G, N, K / 2] 4-bit codes 0..15.  64 consecutive k are 32 bytes, eight
+ *             little-endian words; nibble i of word 2 c + j holds k = 32 j + 8 c + 2 i (i < 4) or
+ *             k = 32 j + 8 c + 2 i - 7 (i >= 4).
+ *   scales    [G, ceil(K / group), N] e4m3 numbers (a last group may be short).
+ *   zeros     [G, ceil(K / group), N] 0..15, or NULL: 8 everywhere.
+ *   row_scale [G, N] fp32.
+ *   group     32, 64 or 128.
+ * scale * (code - zero) has at most 8 significant bits, so it is a bf16 exactly: products with
+ * these weights round nothing before their fp32 sums, which row_scale multiplies at the end. */
+typedef struct moe_w4 {
+    uint8_t* codes;
+    uint8_t* scales;
+    uint8_t* zeros;
+    float* row_scale;
+    int32_t group;
+    int32_t reserved;      /* 0 */
+} moe_w4_t;
+
+/* n_matrices matrices W [N, K] (dtype MOE_BF16 or MOE_F32) to the 4-bit form: all arrays of `out`
+ * are written, with zero points if out->zeros is given.  Per row and group, in fp32:
+ *   t = max|w| / 7, with zero points t = (max(w, 0) - min(w, 0)) / 15;
+ *   row_scale = max_groups t / 448;  scale = e4m3(t / row_scale);  step = scale * row_scale;
+ *   code = clamp(rint(w * (1 / step)), -8, 7) + 8, with zero points
+ *   zero = clamp(rint(-min(w, 0) * (1 / step)), 0, 15) and
+ *   code = clamp(rint(w * (1 / step)) + zero, 0, 15).
+ * A row of zeros (largest t below 2^-100) has row_scale 0; a row that holds a NaN or an infinity
+ * stands for NaN.  moe_dequantize_w4 writes the values W stands for, rounded once to dtype.
+ * 0 <= n_matrices; n_matrices * N < 2^31. */
+moe_status_t moe_quantize_w4(int32_t n_matrices, int32_t N, int32_t K, int32_t dtype,
+                             const void* W, const moe_w4_t* out, moe_stream_t stream);
+moe_status_t moe_dequantize_w4(int32_t n_matrices, int32_t N, int32_t K, const moe_w4_t* w,
+                               int32_t dtype, void* W, moe_stream_t stream);
+
+/* moe_expert_up / moe_expert_down on 4-bit weights: gate, up [n_groups, F, D] (gate NULL for ReLU /
+ * GELU; under SwiGLU of the same group and both with or both without zeros), down
+ * [n_groups, D, F].  a, h, y bf16 (MOE_ERR_UNSUPPORTED for fp32 layers), fp32 sums; the other
+ * arguments and the rows written are those of moe_expert_up / moe_expert_down, and results are
+ * those of the values the weights stand for.  No scratch. */
+moe_status_t moe_expert_up_w4(const moe_desc_t* desc, int32_t n_groups, int32_t F,
+                              const void* a, int64_t a_rows, const int32_t* offsets,
+                              const moe_w4_t* gate, const moe_w4_t* up, void* h,
+                              moe_stream_t stream);
+moe_status_t moe_expert_down_w4(const moe_desc_t* desc, int32_t n_groups, int32_t F,
+                                const void* h, int64_t a_rows, const int32_t* offsets,
+                                const moe_w4_t* down, void* y, moe_stream_t stream);
+
+/* moe_layer_forward with the routed experts' weights in 4 bits; the router and the shared experts
+ * keep bf16 weights.  Same steps, workspace, views and statistics. */
+moe_status_t moe_layer_forward_w4(const moe_desc_t* desc, const void* x, const void* Wg,
+                                  const float* sel_bias, const moe_w4_t* gate,
+                                  const moe_w4_t* up, const moe_w4_t* down, const void* Ws_gate,
+                                  const void* Ws_up, const void* Ws_down, void* out, void* ws,
+                                  size_t ws_bytes, moe_stream_t stream);
+
 /* Expert parallelism ("Top-k 路由" section "通訊拓撲：All-to-All": rows go to the device that
  * holds their expert and their outputs come back, two All-to-All exchanges per layer;
  * "别只比较 Top-k", "两次 All-to-All 是常见 dispatcher 的前向合同").  G ranks, rank r holds the

@@ -6,7 +6,9 @@ missing, every call raises.
 
 The functions keep the C names (moe_route, moe_permute, moe_expert_up, moe_expert_down,
 moe_expert_ffn, moe_expert_up_ws, moe_expert_down_ws, moe_combine, moe_balance_stats,
-moe_layer_forward) and take torch tensors.
+moe_layer_forward; moe_combine_backward, moe_permute_backward; moe_quantize_w4,
+moe_dequantize_w4, moe_expert_up_w4, moe_expert_down_w4, moe_layer_forward_w4) and take torch
+tensors.  W4 holds the tensors of expert weights in 4 bits.
 """
 
 from __future__ import annotations
@@ -24,7 +26,9 @@ __all__ = [
     "moe_expert_down", "moe_expert_ffn", "moe_expert_up_ws", "moe_expert_down_ws",
     "moe_permute_noalloc", "moe_combine", "moe_balance_stats", "moe_layer_backward_ex",
     "moe_expert_up_gather", "gather_fusion",
-    "MoeBwdShared",
+    "MoeBwdShared", "MoeW4", "W4", "empty_w4", "moe_combine_backward", "moe_permute_backward",
+    "moe_quantize_w4", "moe_dequantize_w4", "moe_expert_up_w4", "moe_expert_down_w4",
+    "moe_layer_forward_w4",
     "moe_layer_forward", "get_device_error", "empty_scratch", "empty_workspace",
 ]
 
@@ -77,6 +81,12 @@ class MoeBwdShared(ctypes.Structure):
                 ("dWs_up", ctypes.c_void_p), ("dWs_down", ctypes.c_void_p)]
 
 
+class MoeW4(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("zeros", ctypes.c_void_p), ("row_scale", ctypes.c_void_p),
+                ("group", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, fn, status):
         self.status = status
@@ -89,6 +99,7 @@ _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
 _DP = ctypes.POINTER(MoeDesc)
+_W4P = ctypes.POINTER(MoeW4)
 
 _SIGS = {
     "moe_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -121,6 +132,14 @@ _SIGS = {
                               ctypes.c_int),
     "moe_layer_forward_train": ([_DP, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P, _SZ, _P],
                                 ctypes.c_int),
+    "moe_combine_backward": ([_DP, _P, _P, _P, _P, _P, _P, _P], ctypes.c_int),
+    "moe_permute_backward": ([_DP, _P, _P, _P, _P, _P], ctypes.c_int),
+    "moe_quantize_w4": ([_I32, _I32, _I32, _I32, _P, _W4P, _P], ctypes.c_int),
+    "moe_dequantize_w4": ([_I32, _I32, _I32, _W4P, _I32, _P, _P], ctypes.c_int),
+    "moe_expert_up_w4": ([_DP, _I32, _I32, _P, _I64, _P, _W4P, _W4P, _P, _P], ctypes.c_int),
+    "moe_expert_down_w4": ([_DP, _I32, _I32, _P, _I64, _P, _W4P, _P, _P], ctypes.c_int),
+    "moe_layer_forward_w4": ([_DP, _P, _P, _P, _W4P, _W4P, _W4P, _P, _P, _P, _P, _P, _SZ, _P],
+                             ctypes.c_int),
     "moe_get_device_error": ([_P, ctypes.POINTER(_I32)], ctypes.c_int),
     "moe_debug_inject": ([_I32], ctypes.c_int),
     "moe_kernel_launches": ([], ctypes.c_int64),
@@ -153,7 +172,7 @@ def header_functions(path: str = HEADER):
     with open(path) as f:
         text = f.read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
-    return sorted(set(re.findall(r"\b(moe_[a-z_]+)\s*\(", text)))
+    return sorted(set(re.findall(r"\b(moe_[a-z0-9_]+)\s*\(", text)))
 
 
 def status_string(status: int) -> str:
@@ -415,6 +434,128 @@ def moe_layer_forward_train(d, x, Wg, sel_bias, W_gate, W_up, W_down, out, ws, b
         ctypes.byref(d), _ptr(x), _ptr(Wg), _ptr(sel_bias), _ptr(W_gate), _ptr(W_up),
         _ptr(W_down), _ptr(out), _ptr(ws), ws.numel(), _ptr(bwd_ws), bwd_ws.numel(),
         _stream(stream)))
+
+
+def _here(*tensors):
+    """Refuses tensors that are not on the current CUDA device (None and addresses pass)."""
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and not (
+                t.is_cuda and t.get_device() == torch.cuda.current_device()):
+            raise ValueError(f"a tensor on {t.device} was handed to the MoE library, which runs "
+                             "on the current CUDA device")
+
+
+# ------------------------------------ gradients of the dispatch and merge ----
+
+def moe_combine_backward(d, dout, y, inv, gates, dy, dgates, stream=None):
+    """Gradient of moe_combine: dy (expert output rows) and dgates; either may be None."""
+    _here(dout, y, inv, gates, dy, dgates)
+    _check("moe_combine_backward", lib().moe_combine_backward(
+        ctypes.byref(d), _ptr(dout), _ptr(y), _ptr(inv), _ptr(gates), _ptr(dy), _ptr(dgates),
+        _stream(stream)))
+
+
+def moe_permute_backward(d, dx_perm, inv, add, dx, stream=None):
+    """Gradient of moe_permute: dx = add (or None) + each token's rows of dx_perm."""
+    _here(dx_perm, inv, add, dx)
+    _check("moe_permute_backward", lib().moe_permute_backward(
+        ctypes.byref(d), _ptr(dx_perm), _ptr(inv), _ptr(add), _ptr(dx), _stream(stream)))
+
+
+# --------------------------------------------------- 4-bit expert weights ----
+
+class W4:
+    """Expert weights [G, N, K] in 4 bits with group scales (moe_w4_t in include/moe.h).
+
+    codes [G, N, K / 2] uint8, scales [G, ceil(K / group), N] float8_e4m3fn, zeros (uint8, the
+    shape of scales) or None, row_scale [G, N] fp32; contiguous, on one device.  A single matrix
+    may leave G out."""
+
+    def __init__(self, codes, scales, zeros, row_scale, group):
+        if codes.dim() not in (2, 3) or codes.dtype != torch.uint8:
+            raise ValueError("codes must be uint8 [G, N, K / 2] or [N, K / 2]")
+        lead, N, K = codes.shape[:-2], codes.shape[-2], 2 * codes.shape[-1]
+        if group not in (32, 64, 128):
+            raise ValueError(f"group must be 32, 64 or 128, not {group}")
+        groups = -(-K // group)
+        if scales.dtype != torch.float8_e4m3fn or scales.shape != (*lead, groups, N):
+            raise ValueError(f"scales must be float8_e4m3fn {[*lead, groups, N]}")
+        if zeros is not None and (zeros.dtype != torch.uint8 or zeros.shape != scales.shape):
+            raise ValueError(f"zeros must be uint8 {[*lead, groups, N]}")
+        if row_scale.dtype != torch.float32 or row_scale.shape != (*lead, N):
+            raise ValueError(f"row_scale must be float32 {[*lead, N]}")
+        if len({t.device for t in (codes, scales, zeros, row_scale) if t is not None}) > 1:
+            raise ValueError("the tensors of 4-bit weights must be on one device")
+        self.codes, self.scales, self.zeros, self.row_scale = codes, scales, zeros, row_scale
+        self.group, self.G, self.N, self.K = group, lead[0] if lead else 1, N, K
+        self._c = MoeW4(_ptr(codes), _ptr(scales), _ptr(zeros), _ptr(row_scale), group, 0)
+
+
+def empty_w4(G, N, K, group=128, zeros=False, device="cuda") -> W4:
+    """Unwritten 4-bit weights for moe_quantize_w4."""
+    shape = (G, -(-K // group), N)
+    return W4(torch.empty((G, N, K // 2), dtype=torch.uint8, device=device),
+              torch.empty(shape, dtype=torch.float8_e4m3fn, device=device),
+              torch.empty(shape, dtype=torch.uint8, device=device) if zeros else None,
+              torch.empty((G, N), dtype=torch.float32, device=device), group)
+
+
+def _w4(w, G, N, K, what):
+    if w is None:
+        return None
+    if (w.G, w.N, w.K) != (G, N, K):
+        raise ValueError(f"{what} holds [{w.G}, {w.N}, {w.K}], not [{G}, {N}, {K}]")
+    _here(w.codes)
+    return ctypes.byref(w._c)
+
+
+def _w4_wide(W, w):
+    if W.numel() != w.G * w.N * w.K or W.shape[-1] != w.K:
+        raise ValueError(f"W {list(W.shape)} does not match 4-bit [{w.G}, {w.N}, {w.K}]")
+    if W.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"W must be float32 or bfloat16, not {W.dtype}")
+    return F32 if W.dtype == torch.float32 else BF16
+
+
+def moe_quantize_w4(W, w, stream=None):
+    """Writes the 4-bit form of W [G, N, K] (fp32 or bf16) to the tensors of w (a W4)."""
+    dt = _w4_wide(W, w)
+    _here(W, w.codes)
+    _check("moe_quantize_w4", lib().moe_quantize_w4(
+        w.G, w.N, w.K, dt, _ptr(W), ctypes.byref(w._c), _stream(stream)))
+
+
+def moe_dequantize_w4(w, W, stream=None):
+    """Writes the values that w (a W4) stands for to W [G, N, K] (fp32 or bf16)."""
+    dt = _w4_wide(W, w)
+    _here(W, w.codes)
+    _check("moe_dequantize_w4", lib().moe_dequantize_w4(
+        w.G, w.N, w.K, ctypes.byref(w._c), dt, _ptr(W), _stream(stream)))
+
+
+def moe_expert_up_w4(d, n_groups, F, a, offsets, gate, up, h, stream=None):
+    _here(a, offsets, h)
+    _check("moe_expert_up_w4", lib().moe_expert_up_w4(
+        ctypes.byref(d), n_groups, F, _ptr(a), a.shape[0], _ptr(offsets),
+        _w4(gate, n_groups, F, d.D, "gate"), _w4(up, n_groups, F, d.D, "up"), _ptr(h),
+        _stream(stream)))
+
+
+def moe_expert_down_w4(d, n_groups, F, h, offsets, down, y, stream=None):
+    _here(h, offsets, y)
+    _check("moe_expert_down_w4", lib().moe_expert_down_w4(
+        ctypes.byref(d), n_groups, F, _ptr(h), h.shape[0], _ptr(offsets),
+        _w4(down, n_groups, d.D, F, "down"), _ptr(y), _stream(stream)))
+
+
+def moe_layer_forward_w4(d, x, Wg, sel_bias, gate, up, down, Ws_gate, Ws_up, Ws_down, out, ws,
+                         stream=None):
+    """moe_layer_forward with the routed experts' weights as W4 (gate None unless SwiGLU)."""
+    _here(x, Wg, sel_bias, Ws_gate, Ws_up, Ws_down, out, ws)
+    _check("moe_layer_forward_w4", lib().moe_layer_forward_w4(
+        ctypes.byref(d), _ptr(x), _ptr(Wg), _ptr(sel_bias), _w4(gate, d.E, d.F, d.D, "gate"),
+        _w4(up, d.E, d.F, d.D, "up"), _w4(down, d.E, d.D, d.F, "down"), _ptr(Ws_gate),
+        _ptr(Ws_up), _ptr(Ws_down), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
 
 
 def get_device_error(stream=None) -> int:

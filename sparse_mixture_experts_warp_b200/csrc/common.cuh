@@ -230,6 +230,27 @@ cudaError_t launch_dx(const void* dX, const int32_t* inv, const float* ds, const
 cudaError_t launch_dwg(const float* ds, const void* x, int T, int D, int E, float* part,
                        float* dWg, cudaStream_t s);
 
+// step_backward.cu: the gradients of the merge (dy and / or dgates, either may be null) and of
+// the dispatch (add may be null) as steps of their own
+cudaError_t launch_combine_backward(const moe_desc_t& d, const void* dout, const void* y,
+                                    const int32_t* inv, const float* gates, void* dy,
+                                    float* dgates, cudaStream_t s);
+cudaError_t launch_permute_backward(const moe_desc_t& d, const void* dx_perm,
+                                    const int32_t* inv, const void* add, void* dx,
+                                    cudaStream_t s);
+
+// w4_convert.cu: expert weights to and from the 4-bit form (w4.cuh)
+cudaError_t launch_quantize_w4(int n_matrices, int N, int K, bool bf16, const void* W,
+                               const moe_w4_t& o, cudaStream_t s);
+cudaError_t launch_dequantize_w4(int n_matrices, int N, int K, const moe_w4_t& w, bool bf16,
+                                 void* out, cudaStream_t s);
+// w4_product.cu: out[r, n] = act(sum_k a[r, k] W_g[n, k]) for the rows r of group g, or
+// SiLU(gate) * up with gate != null; act: MOE_ACT_* or -1 (none: the down projection).  bf16 a
+// [a_rows, K] and out [a_rows, N].
+cudaError_t launch_w4_product(int act, const void* a, int64_t a_rows, int K, const moe_w4_t* gate,
+                              const moe_w4_t* w, int G, int N, const int32_t* offsets, void* out,
+                              cudaStream_t s);
+
 // Test hook of the grouped GEMM's bounded waits (see moe_debug_inject).
 void set_gemm_fault(int kind);
 

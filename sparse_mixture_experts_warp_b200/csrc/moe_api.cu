@@ -681,11 +681,116 @@ moe_status_t moe_balance_stats(const moe_desc_t* d, const int32_t* counts, const
                                           reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// ---- gradients of the dispatch and of the merge ----
+
+moe_status_t moe_combine_backward(const moe_desc_t* d, const void* dout, const void* y,
+                                  const int32_t* inv, const float* gates, void* dy,
+                                  float* dgates, moe_stream_t stream) {
+  moe_status_t st = validate(d);
+  if (st != MOE_OK) return st;
+  if (!dout || !inv || !gates || (!dy && !dgates) || (dgates && !y)) return MOE_ERR_INVALID_ARG;
+  if (!is_aligned16(dout) || !is_aligned16(y) || !is_aligned16(inv) || !is_aligned16(gates) ||
+      !is_aligned16(dy) || !is_aligned16(dgates))
+    return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_combine_backward(*d, dout, y, inv, gates, dy, dgates,
+                                             reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_permute_backward(const moe_desc_t* d, const void* dx_perm, const int32_t* inv,
+                                  const void* add, void* dx, moe_stream_t stream) {
+  moe_status_t st = validate(d);
+  if (st != MOE_OK) return st;
+  if (!dx_perm || !inv || !dx) return MOE_ERR_INVALID_ARG;
+  if (!is_aligned16(dx_perm) || !is_aligned16(inv) || !is_aligned16(add) || !is_aligned16(dx))
+    return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_permute_backward(*d, dx_perm, inv, add, dx,
+                                             reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// ---- 4-bit expert weights ----
+
+static moe_status_t check_w4(const moe_w4_t* w) {
+  if (!w || !w->codes || !w->scales || !w->row_scale) return MOE_ERR_INVALID_ARG;
+  if (!is_aligned16(w->codes) || !is_aligned16(w->scales) || !is_aligned16(w->zeros) ||
+      !is_aligned16(w->row_scale))
+    return MOE_ERR_INVALID_ARG;
+  if (w->reserved != 0) return MOE_ERR_INVALID_ARG;
+  if (w->group != 32 && w->group != 64 && w->group != 128) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+static moe_status_t check_w4_convert(int32_t n, int32_t N, int32_t K, int32_t dtype,
+                                     const void* W, const moe_w4_t* w) {
+  if (n < 0 || N <= 0 || K <= 0 || !W || !is_aligned16(W)) return MOE_ERR_INVALID_ARG;
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  const moe_status_t st = check_w4(w);
+  if (st != MOE_OK) return st;
+  if (N % 64 || K % 64 || (int64_t)n * N >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status_t moe_quantize_w4(int32_t n, int32_t N, int32_t K, int32_t dtype, const void* W,
+                             const moe_w4_t* out, moe_stream_t stream) {
+  const moe_status_t st = check_w4_convert(n, N, K, dtype, W, out);
+  if (st != MOE_OK || n == 0) return st;
+  return cuda_status(launch_quantize_w4(n, N, K, dtype == MOE_BF16, W, *out,
+                                        reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_dequantize_w4(int32_t n, int32_t N, int32_t K, const moe_w4_t* w, int32_t dtype,
+                               void* W, moe_stream_t stream) {
+  const moe_status_t st = check_w4_convert(n, N, K, dtype, W, w);
+  if (st != MOE_OK || n == 0) return st;
+  return cuda_status(launch_dequantize_w4(n, N, K, *w, dtype == MOE_BF16, W,
+                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
+static moe_status_t check_w4_up(const moe_desc_t* d, const moe_w4_t* gate, const moe_w4_t* up) {
+  if (d->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  moe_status_t st = check_w4(up);
+  if (st != MOE_OK || d->act != MOE_ACT_SWIGLU) return st;
+  st = check_w4(gate);
+  if (st != MOE_OK) return st;
+  if (gate->group != up->group || !gate->zeros != !up->zeros) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status_t moe_expert_up_w4(const moe_desc_t* d, int32_t G, int32_t F, const void* a,
+                              int64_t a_rows, const int32_t* offsets, const moe_w4_t* gate,
+                              const moe_w4_t* up, void* h, moe_stream_t stream) {
+  moe_status_t st = check_ffn(d, G, F, a, a_rows, offsets);
+  if (st != MOE_OK) return st;
+  st = check_w4_up(d, gate, up);
+  if (st != MOE_OK) return st;
+  if (!h || !is_aligned16(h)) return MOE_ERR_INVALID_ARG;
+  const bool glu = d->act == MOE_ACT_SWIGLU;
+  return cuda_status(launch_w4_product(d->act, a, a_rows, d->D, glu ? gate : nullptr, up, G, F,
+                                       offsets, h, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_expert_down_w4(const moe_desc_t* d, int32_t G, int32_t F, const void* h,
+                                int64_t a_rows, const int32_t* offsets, const moe_w4_t* down,
+                                void* y, moe_stream_t stream) {
+  moe_status_t st = check_ffn(d, G, F, h, a_rows, offsets);
+  if (st != MOE_OK) return st;
+  if (d->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  st = check_w4(down);
+  if (st != MOE_OK) return st;
+  if (!y || !is_aligned16(y)) return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_w4_product(-1, h, a_rows, F, nullptr, down, G, d->D, offsets, y,
+                                       reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// The routed experts' weights in 4 bits (moe_layer_forward_w4).
+struct W4Experts {
+  const moe_w4_t *gate, *up, *down;
+};
+
 static moe_status_t forward_impl(const moe_desc_t* d, const void* x, const void* Wg,
                                  const float* sel_bias, const void* W_gate, const void* W_up,
                                  const void* W_down, const void* Ws_gate, const void* Ws_up,
                                  const void* Ws_down, void* out, void* ws, size_t ws_bytes,
-                                 void* preact, moe_stream_t stream);
+                                 void* preact, const W4Experts* w4, moe_stream_t stream);
 
 moe_status_t moe_layer_forward(const moe_desc_t* d, const void* x, const void* Wg,
                                const float* sel_bias, const void* W_gate, const void* W_up,
@@ -693,21 +798,38 @@ moe_status_t moe_layer_forward(const moe_desc_t* d, const void* x, const void* W
                                const void* Ws_down, void* out, void* ws, size_t ws_bytes,
                                moe_stream_t stream) {
   return forward_impl(d, x, Wg, sel_bias, W_gate, W_up, W_down, Ws_gate, Ws_up, Ws_down, out,
-                      ws, ws_bytes, nullptr, stream);
+                      ws, ws_bytes, nullptr, nullptr, stream);
+}
+
+moe_status_t moe_layer_forward_w4(const moe_desc_t* d, const void* x, const void* Wg,
+                                  const float* sel_bias, const moe_w4_t* gate,
+                                  const moe_w4_t* up, const moe_w4_t* down, const void* Ws_gate,
+                                  const void* Ws_up, const void* Ws_down, void* out, void* ws,
+                                  size_t ws_bytes, moe_stream_t stream) {
+  moe_status_t st = validate(d);
+  if (st != MOE_OK) return st;
+  st = check_w4_up(d, gate, up);
+  if (st != MOE_OK) return st;
+  st = check_w4(down);
+  if (st != MOE_OK) return st;
+  const W4Experts w4{gate, up, down};
+  return forward_impl(d, x, Wg, sel_bias, nullptr, nullptr, nullptr, Ws_gate, Ws_up, Ws_down, out,
+                      ws, ws_bytes, nullptr, &w4, stream);
 }
 
 // preact != nullptr (bf16 token choice, from moe_layer_forward_train): the routed up
-// projection also stores its raw accumulators there for the backward pass.
+// projection also stores its raw accumulators there for the backward pass.  w4 != nullptr (bf16,
+// checked by the caller): the routed experts' weights in 4 bits instead of W_gate, W_up, W_down.
 static moe_status_t forward_impl(const moe_desc_t* d, const void* x, const void* Wg,
                                  const float* sel_bias, const void* W_gate, const void* W_up,
                                  const void* W_down, const void* Ws_gate, const void* Ws_up,
                                  const void* Ws_down, void* out, void* ws, size_t ws_bytes,
-                                 void* preact, moe_stream_t stream) {
+                                 void* preact, const W4Experts* w4, moe_stream_t stream) {
   moe_layer_views_t v;
   moe_status_t st = moe_layer_views(d, ws, ws_bytes, &v);
   if (st != MOE_OK) return st;
-  if (!x || !Wg || !W_up || !W_down || !out) return MOE_ERR_INVALID_ARG;
-  if (d->act == MOE_ACT_SWIGLU && !W_gate) return MOE_ERR_INVALID_ARG;
+  if (!x || !Wg || !out || (!w4 && (!W_up || !W_down))) return MOE_ERR_INVALID_ARG;
+  if (!w4 && d->act == MOE_ACT_SWIGLU && !W_gate) return MOE_ERR_INVALID_ARG;
   if (d->n_shared > 0 && (!Ws_gate || !Ws_up || !Ws_down)) return MOE_ERR_INVALID_ARG;
   if (d->T == 0) return MOE_OK;
   st = moe_route(d, x, Wg, sel_bias, v.expert_ids, v.gates, v.logits, v.importance, v.entropy,
@@ -716,7 +838,7 @@ static moe_status_t forward_impl(const moe_desc_t* d, const void* x, const void*
   // with enough rows (bf16), the up projection gathers the token rows itself and the
   // permutation writes indices only
   int32_t gather = 0;
-  if (!preact) moe_gather_fusion(d, &gather);
+  if (!preact && !w4) moe_gather_fusion(d, &gather);
   st = moe_permute(d, v.expert_ids, x, gather ? nullptr : v.x_perm, v.counts, v.offsets,
                    v.row_src, v.inv, v.scratch, v.scratch_bytes, stream);
   if (st != MOE_OK) return st;
@@ -724,7 +846,12 @@ static moe_status_t forward_impl(const moe_desc_t* d, const void* x, const void*
   // itself (one launch fewer)
   SplitRows split{};
   SplitRows* defer = d->n_shared == 0 ? &split : nullptr;
-  if (gather) {
+  if (w4) {
+    st = moe_expert_up_w4(d, d->E, d->F, v.x_perm, v.rows, v.offsets, w4->gate, w4->up, v.h,
+                          stream);
+    if (st == MOE_OK)
+      st = moe_expert_down_w4(d, d->E, d->F, v.h, v.rows, v.offsets, w4->down, v.y, stream);
+  } else if (gather) {
     st = moe_expert_up_gather(d, d->E, d->F, x, v.row_src, v.rows, v.offsets, W_gate, W_up, v.h,
                               stream);
     if (st == MOE_OK)
@@ -936,7 +1063,7 @@ moe_status_t moe_layer_forward_train(const moe_desc_t* d, const void* x, const v
   if ((reinterpret_cast<uintptr_t>(bwd_ws) % kAlign) != 0) return MOE_ERR_WORKSPACE;
   carve_bwd(d, static_cast<uint8_t*>(bwd_ws), &b);
   return forward_impl(d, x, Wg, sel_bias, W_gate, W_up, W_down, nullptr, nullptr, nullptr, out,
-                      ws, ws_bytes, b.gu, stream);
+                      ws, ws_bytes, b.gu, nullptr, stream);
 }
 
 moe_status_t moe_layer_backward(const moe_desc_t* d, const void* x, const void* Wg,
