@@ -251,8 +251,14 @@ cudaError_t launch_w4_product(int act, const void* a, int64_t a_rows, int K, con
                               const moe_w4_t* w, int G, int N, const int32_t* offsets, void* out,
                               cudaStream_t s);
 
+// w4_gemm.cu: the same product on tcgen05, for any number of rows
+cudaError_t launch_w4_gemm(int act, const void* a, int64_t a_rows, int K, const moe_w4_t* gate,
+                           const moe_w4_t* w, int G, int N, const int32_t* offsets, void* out,
+                           cudaStream_t s);
+
 // Test hook of the grouped GEMM's bounded waits (see moe_debug_inject).
 void set_gemm_fault(int kind);
+int gemm_fault();
 
 // backward_f32.cu (fp32 layer backward on CUDA cores)
 size_t backward_f32_workspace(const moe_desc_t& d, int64_t rows);

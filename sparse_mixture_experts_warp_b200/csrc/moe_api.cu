@@ -764,7 +764,7 @@ moe_status_t moe_expert_up_w4(const moe_desc_t* d, int32_t G, int32_t F, const v
   if (st != MOE_OK) return st;
   if (!h || !is_aligned16(h)) return MOE_ERR_INVALID_ARG;
   const bool glu = d->act == MOE_ACT_SWIGLU;
-  return cuda_status(launch_w4_product(d->act, a, a_rows, d->D, glu ? gate : nullptr, up, G, F,
+  return cuda_status(launch_w4_gemm(d->act, a, a_rows, d->D, glu ? gate : nullptr, up, G, F,
                                        offsets, h, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -777,7 +777,7 @@ moe_status_t moe_expert_down_w4(const moe_desc_t* d, int32_t G, int32_t F, const
   st = check_w4(down);
   if (st != MOE_OK) return st;
   if (!y || !is_aligned16(y)) return MOE_ERR_INVALID_ARG;
-  return cuda_status(launch_w4_product(-1, h, a_rows, F, nullptr, down, G, d->D, offsets, y,
+  return cuda_status(launch_w4_gemm(-1, h, a_rows, F, nullptr, down, G, d->D, offsets, y,
                                        reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -135,5 +135,9 @@ __device__ __forceinline__ int ld_cluster_s32(uint32_t cl_addr) {
 // 128-byte swizzle for kb = 64, 64-byte for kb = 32; rows past the end read as zeros.
 bool make_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows,
               int kb);
+// Host: 2-D byte tensor map [rows, cols] (row-major, cols a multiple of 16), box = box_cols bytes
+// x box_rows rows, 128-byte swizzle (box_cols = 128) or none; parts past the end read as zeros.
+bool make_map_u8(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows,
+                 uint32_t box_cols, bool swizzle);
 
 }  // namespace moe

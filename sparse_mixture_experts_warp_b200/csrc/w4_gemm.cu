@@ -1,0 +1,655 @@
+// Grouped product on 4-bit weights (w4.cuh) with tcgen05: the weights are dequantised into
+// tensor memory and feed the MMA from there.
+//
+// "从 Dense FFN 到 MoE：用一个 Tiny Transformer 理解 Router、Top-K 与负载均衡" (f3dlife), section 3
+// (SwiGLU expert: hidden = SiLU(x W_gate) * (x W_up), output = hidden W_down); "别只比较 Top-k"
+// (ailearn moe-comparison), the Execute step.
+//
+// out[r, n] = epi(row_scale[n] * sum_k scale[k / g, n] (code[n, k] - zero[k / g, n]) a[r, k]) for
+// the rows r of group g.  The weights are the MMA's M side and the tokens its N side:
+//   D[n, t] = sum_k w[n, k] a[row0 + t, k]       (TMEM lane = weight row, column = token)
+// so one thread owns one weight row: its codes, its group scales, its row factor, and its lane of
+// the A operand.  scale * (code - zero) is a bf16 exactly, so nothing is rounded on the way in.
+// A tile is 128 weight rows by up to NT tokens of one group; N of the MMA is the token count
+// rounded up to 16.  SwiGLU: lanes 0..15 of every 32 hold 16 rows of W_gate, lanes 16..31 the
+// same rows of W_up, so gate and up of a feature are one warp shuffle apart.
+//
+// Roles (one persistent CTA per SM; tiles group by group, weight tile by weight tile, token tiles
+// innermost, so that the CTAs that run together share weight tiles through L2):
+//   warp 0       TMA producer of the weights: 256 k of codes (128 rows x 128 bytes, 128-byte
+//                swizzle: a thread's 16-byte reads of its row are free of bank conflicts), and
+//                their scales and zero points, per stage;
+//   warp 1       TMA producer of the token rows: 64 k (NT = 256) to 256 k (NT = 32) per stage, in
+//                boxes of 64 k (128-byte swizzle);
+//   warp 2       MMA issuer (tcgen05.mma kind::f16, A from tensor memory) and TMEM owner;
+//   warp 3       group table;
+//   warps 4..    dequantisers: 4 * W4_DQ_SETS warps, each set of four takes every W4_DQ_SETS-th
+//                128-element k-block, thread by thread 16 words -> 64 columns of packed bf16
+//                pairs (tcgen05.st), into a ring of 4 A stages of 64 columns;
+//   then         epilogue: tcgen05.ld, row factor, activation, bf16 stores.
+// TMEM: 256 accumulator columns (one tile of up to 256 tokens, or two of up to 128 so that the
+// epilogue of a tile overlaps the next one's main loop) and 4 x 64 columns of A.
+// When few tokens share a weight the loop has to run at the rate of the weights' bytes (a stage
+// of 16 KB of codes every 0.4 us), so stages are as long as memory allows: at 64-element A and
+// token stages the barrier traffic of the one MMA thread alone took 1.2 us for 16 KB.
+// Every mbarrier wait is bounded (globaltimer); a wait that gives up records an error code in
+// the device error word and the CTA drains what it has in flight and exits.
+#include <cuda.h>
+
+#include "common.cuh"
+#include "mbar.cuh"
+#include "tc_ops.cuh"
+#include "w4.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int W4_ROWS = 128;                    // weight rows of a tile (TMEM lanes)
+constexpr int W4_KS = 256;                      // k of a weight stage
+constexpr int W4_KB = 64;                       // k of a token box
+constexpr int W4_KA = 128;                      // k of an A stage
+constexpr int W4_CODE_BYTES = W4_ROWS * W4_KS / 2;
+constexpr int W4_SIDE_BYTES = 1024;             // scales (or zero points) of a stage: 8 x 128
+constexpr int W4_W_STAGE = W4_CODE_BYTES + 2 * W4_SIDE_BYTES;
+constexpr int W4_XBOX = 32;                     // token rows per box
+constexpr int W4_XBOX_BYTES = W4_XBOX * W4_KB * 2;
+constexpr int W4_A_STAGES = 4;
+constexpr int W4_A_COLS = W4_KA / 2;
+constexpr int W4_ACC_COLS = 256;
+constexpr int W4_TMEM_COLS = 512;
+constexpr int W4_DQ_SETS = 2;
+constexpr int W4_EPI_SETS = 2;
+constexpr int W4_FIRST_DQ = 4;
+constexpr int W4_FIRST_EPI = W4_FIRST_DQ + 4 * W4_DQ_SETS;
+constexpr int W4_THREADS = 32 * (W4_FIRST_EPI + 4 * W4_EPI_SETS);
+constexpr uint64_t W4_TIMEOUT_NS = 2000000000ull;   // 2 s per wait
+constexpr uint64_t W4_DRAIN_NS = 200000000ull;      // 0.2 s to drain after an abort
+constexpr unsigned kFull = 0xffffffffu;
+
+// Tokens of a tile, weight stages, token stages and their k, accumulators.
+template <int NT> struct W4Shape;
+template <> struct W4Shape<256> { static constexpr int WS = 3, XS = 5, XK = 64, ACCS = 1; };
+template <> struct W4Shape<128> { static constexpr int WS = 5, XS = 3, XK = 128, ACCS = 2; };
+template <> struct W4Shape<32> { static constexpr int WS = 8, XS = 4, XK = 256, ACCS = 2; };
+
+struct W4Params {
+  const int32_t* offsets;                       // [G + 1] device
+  const float* rs0;                             // row factors [G, N]: up / down
+  const float* rs1;                             // gate (SwiGLU)
+  __nv_bfloat16* out;                           // [rows, N]
+  int* err;
+  int64_t rows;
+  int G, N, K, group;
+  int act;                                      // MOE_ACT_* or -1
+  int zeros;
+  int nt;                                       // weight tiles per group
+  int fault;                                    // test hook: CTA 0 arms its first weight stage only
+};
+
+struct W4Tile {
+  int g, n_idx, ntok, row0;
+};
+
+template <int NT>
+__device__ __forceinline__ W4Tile w4_locate(int t, const int* grp_off, const int* tile_pre,
+                                            int& g) {
+  while (t >= tile_pre[g + 1]) ++g;
+  const int m = grp_off[g + 1] - grp_off[g];
+  const int mt = (m + NT - 1) / NT;
+  const int local = t - tile_pre[g];
+  W4Tile r;
+  r.g = g;
+  r.n_idx = local / mt;
+  const int j = local - r.n_idx * mt;
+  r.ntok = min(NT, m - j * NT);
+  r.row0 = grp_off[g] + j * NT;
+  return r;
+}
+
+// Barrier steps on shared-memory addresses.  The common case of a wait, a phase that has passed,
+// is inline: through mbar_wait's call the MMA thread ran a quarter slower.
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+struct W4Wait {
+  volatile int* abort_flag;
+  int* err;
+  // one thread
+  __device__ __forceinline__ bool one(uint32_t bar, uint32_t parity, int code) const {
+    if (bar_try(bar, parity)) return true;
+    return mbar_wait(static_cast<uint64_t*>(__cvta_shared_to_generic(bar)), parity, abort_flag,
+                     err, code, W4_TIMEOUT_NS);
+  }
+  // a whole warp: one try by all lanes, then lane 0 polls
+  __device__ __forceinline__ bool warp(uint32_t bar, uint32_t parity, int code, int lane) const {
+    if (__all_sync(kFull, bar_try(bar, parity))) return true;
+    int ok = 1;
+    if (lane == 0)
+      ok = mbar_wait(static_cast<uint64_t*>(__cvta_shared_to_generic(bar)), parity, abort_flag,
+                     err, code, W4_TIMEOUT_NS);
+    return __shfl_sync(kFull, ok, 0) != 0;
+  }
+  // copies or MMAs in flight, before the CTA exits
+  __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, int code,
+                                        uint64_t limit) const {
+    mbar_wait(static_cast<uint64_t*>(__cvta_shared_to_generic(bar)), parity, abort_flag, err,
+              code, limit, /*honor_abort=*/false);
+  }
+};
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bar_commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void bar_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
+                                         int y) {
+  tma_load_2d(dst, map, static_cast<uint64_t*>(__cvta_shared_to_generic(bar)), x, y);
+}
+
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
+                                             uint32_t acc, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ uint32_t bits(__nv_bfloat162 v) {
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+__device__ __forceinline__ __nv_bfloat162 pair(uint32_t v) {
+  return *reinterpret_cast<__nv_bfloat162*>(&v);
+}
+
+// Eight weights of a word as four bf16 pairs: (128 + code) by bits, minus (128 + zero), times
+// scale; every step is exact.
+__device__ __forceinline__ void dequant_word(uint32_t w, __nv_bfloat162 z, __nv_bfloat162 s,
+                                             uint32_t* r) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    r[i] = bits(__hmul2(__hsub2(pair(((w >> (4 * i)) & 0x000f000fu) | 0x43004300u), z), s));
+}
+
+template <int NT, bool GLU>
+__global__ void __launch_bounds__(W4_THREADS, 1)
+w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmC0,
+               const __grid_constant__ CUtensorMap tmC1, const __grid_constant__ CUtensorMap tmS0,
+               const __grid_constant__ CUtensorMap tmS1, const __grid_constant__ CUtensorMap tmZ0,
+               const __grid_constant__ CUtensorMap tmZ1, const W4Params p) {
+  constexpr int WS = W4Shape<NT>::WS, XS = W4Shape<NT>::XS, XK = W4Shape<NT>::XK,
+                ACCS = W4Shape<NT>::ACCS;
+  constexpr int XB = XK / W4_KB;                // 64-element boxes of a token stage
+  constexpr int X_BOX = NT * W4_KB * 2;
+  constexpr int X_STAGE = XB * X_BOX;
+  constexpr int FEATS = GLU ? 64 : 128;         // outputs of a tile
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* ws = smem + XS * X_STAGE;            // token stages, then weight stages
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ws + WS * W4_W_STAGE);
+  constexpr int BARS = 2 * (WS + XS + W4_A_STAGES + ACCS) + 1;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + BARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  int* grp_off = reinterpret_cast<int*>(tmem_holder + 2);       // [G + 1]
+  int* tile_pre = grp_off + (p.G + 1);                          // [G + 1]
+  const uint32_t xs = smem_u32(smem);
+  const uint32_t w_full = smem_u32(bars), w_empty = w_full + 8 * WS;
+  const uint32_t x_full = w_empty + 8 * WS, x_empty = x_full + 8 * XS;
+  const uint32_t a_full = x_empty + 8 * XS, a_empty = a_full + 8 * W4_A_STAGES;
+  const uint32_t t_full = a_empty + 8 * W4_A_STAGES, t_empty = t_full + 8 * ACCS;
+  const uint32_t drain = t_empty + 8 * ACCS;
+  const W4Wait wait{abort_flag, p.err};
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    uint64_t* b = bars;
+    auto init = [&](int n, uint32_t count) {
+      for (int i = 0; i < n; ++i) mbar_init(b++, count);
+    };
+    init(WS, 1);
+    init(WS, 4 * W4_DQ_SETS);
+    init(2 * XS, 1);
+    init(W4_A_STAGES, 4);
+    init(W4_A_STAGES, 1);
+    init(ACCS, 1);
+    init(ACCS, 4 * W4_EPI_SETS);
+    init(1, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_holder)),
+                 "r"(W4_TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  pdl_trigger();
+  pdl_wait();
+  if (warp == 3) {
+    // group row starts and the tile prefix
+    int carry = 0;
+    if (lane == 0) {
+      grp_off[0] = p.offsets[0];
+      tile_pre[0] = 0;
+    }
+    for (int g0 = 0; g0 < p.G; g0 += 32) {
+      const int g = g0 + lane;
+      int tiles = 0;
+      if (g < p.G) {
+        const int lo = p.offsets[g], hi = p.offsets[g + 1];
+        const int m = hi > lo ? hi - lo : 0;
+        tiles = ((m + NT - 1) / NT) * p.nt;
+        grp_off[g + 1] = hi;
+      }
+      int inc = tiles;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kFull, inc, o);
+        if (lane >= o) inc += v;
+      }
+      if (g < p.G) tile_pre[g + 1] = carry + inc;
+      carry += __shfl_sync(kFull, inc, 31);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  const int total = tile_pre[p.G];
+  const int nkb = p.K / W4_KB;                  // 64-element k-blocks
+  const int nws = (nkb + 3) / 4;
+  const int gs = W4_KS / p.group;               // scale rows of a weight stage
+  const int groups = (p.K + p.group - 1) / p.group;
+
+  if (warp == 0) {
+    // ---------------- weights ----------------
+    if (lane == 0) {
+      int stage = 0, g = 0;
+      uint32_t phase = 0, issued = 0, issued_par = 0;
+      bool ok = true;
+      // a box moves its full size, parts outside the tensor as zeros
+      const uint32_t tx = W4_CODE_BYTES + gs * W4_ROWS * (p.zeros ? 2 : 1);
+      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        const W4Tile tl = w4_locate<NT>(t, grp_off, tile_pre, g);
+        const int n0 = tl.n_idx * FEATS, row = tl.g * p.N + n0;
+        for (int s = 0; s < nws; ++s) {
+          if (!wait.one(w_empty + 8 * stage, phase ^ 1u, DEVERR_TIMEOUT_TMA)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar = w_full + 8 * stage;
+          bar_expect(bar, tx);
+          // test hook: the stage is armed but never loaded, so the dequantisers' wait runs out
+          if (!(p.fault == 1 && blockIdx.x == 0 && t == (int)blockIdx.x && s == 0)) {
+            const uint32_t c = xs + XS * X_STAGE + stage * W4_W_STAGE, sc = c + W4_CODE_BYTES,
+                           z = sc + W4_SIDE_BYTES;
+            const int kx = s * (W4_KS / 2), ky = tl.g * groups + s * gs;
+            if (GLU) {
+              bar_load(c, &tmC1, bar, kx, row);
+              bar_load(c + W4_CODE_BYTES / 2, &tmC0, bar, kx, row);
+              bar_load(sc, &tmS1, bar, n0, ky);
+              bar_load(sc + W4_SIDE_BYTES / 2, &tmS0, bar, n0, ky);
+              if (p.zeros) {
+                bar_load(z, &tmZ1, bar, n0, ky);
+                bar_load(z + W4_SIDE_BYTES / 2, &tmZ0, bar, n0, ky);
+              }
+            } else {
+              bar_load(c, &tmC0, bar, kx, row);
+              bar_load(sc, &tmS0, bar, n0, ky);
+              if (p.zeros) bar_load(z, &tmZ0, bar, n0, ky);
+            }
+            issued |= 1u << stage;
+            issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+          }
+          if (++stage == WS) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // the last copies land before the CTA exits, whatever became of their consumers
+      for (int s = 0; s < WS; ++s)
+        if (issued & (1u << s))
+          wait.drain(w_full + 8 * s, (issued_par >> s) & 1u, DEVERR_TIMEOUT_TMA, W4_DRAIN_NS);
+    }
+  } else if (warp == 1) {
+    // ---------------- token rows ----------------
+    if (lane == 0) {
+      int stage = 0, g = 0;
+      uint32_t phase = 0, issued = 0, issued_par = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        const W4Tile tl = w4_locate<NT>(t, grp_off, tile_pre, g);
+        const int nbox = (tl.ntok + W4_XBOX - 1) / W4_XBOX;
+        for (int kb = 0; kb < nkb; kb += XB) {
+          if (!wait.one(x_empty + 8 * stage, phase ^ 1u, DEVERR_TIMEOUT_TMA)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar = x_full + 8 * stage;
+          const int here = min(XB, nkb - kb);
+          bar_expect(bar, here * nbox * W4_XBOX_BYTES);
+          for (int h = 0; h < here; ++h)
+            for (int b = 0; b < nbox; ++b)
+              bar_load(xs + stage * X_STAGE + h * X_BOX + b * W4_XBOX_BYTES, &tmX, bar,
+                       (kb + h) * W4_KB, tl.row0 + b * W4_XBOX);
+          issued |= 1u << stage;
+          issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+          if (++stage == XS) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      for (int s = 0; s < XS; ++s)
+        if (issued & (1u << s))
+          wait.drain(x_full + 8 * s, (issued_par >> s) & 1u, DEVERR_TIMEOUT_TMA, W4_DRAIN_NS);
+    }
+  } else if (warp == 2) {
+    // ---------------- MMA issuer ----------------
+    if (lane == 0) {
+      int xst = 0, ast = 0, it = 0, g = 0;
+      uint32_t xph = 0, aph = 0;
+      bool ok = true;
+      const uint64_t bdesc = sdesc<W4_KB>(xs);
+      for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++it) {
+        const W4Tile tl = w4_locate<NT>(t, grp_off, tile_pre, g);
+        const uint32_t idesc = idesc_bf16(W4_ROWS, (tl.ntok + 15) & ~15);
+        const int acc = it % ACCS;
+        const uint32_t d = tmem_base + acc * (W4_ACC_COLS / ACCS);
+        if (!wait.one(t_empty + 8 * acc, (uint32_t)((it / ACCS) & 1) ^ 1u, DEVERR_TIMEOUT_MMA)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        for (int kb = 0; kb < nkb && ok; kb += W4_KA / W4_KB) {
+          if (!wait.one(a_full + 8 * ast, aph, DEVERR_TIMEOUT_MMA)) {
+            ok = false;
+            break;
+          }
+          const uint32_t a0 = tmem_base + W4_ACC_COLS + ast * W4_A_COLS;
+#pragma unroll
+          for (int h = 0; h < W4_KA / W4_KB; ++h) {
+            if (kb + h >= nkb) break;
+            const int xb = (kb + h) % XB;       // box within the token stage
+            if (xb == 0 && !wait.one(x_full + 8 * xst, xph, DEVERR_TIMEOUT_MMA)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t b = bdesc + (uint32_t)((xst * X_STAGE + xb * X_BOX) >> 4);
+#pragma unroll
+            for (int k = 0; k < W4_KB / 16; ++k)
+              umma_bf16_ts(d, a0 + h * (W4_KB / 2) + 8 * k, b + 2 * k, (kb | h | k) ? 1u : 0u,
+                           idesc);
+            if (xb == XB - 1 || kb + h == nkb - 1) {
+              bar_commit(x_empty + 8 * xst);
+              if (++xst == XS) {
+                xst = 0;
+                xph ^= 1u;
+              }
+            }
+          }
+          bar_commit(a_empty + 8 * ast);
+          if (++ast == W4_A_STAGES) {
+            ast = 0;
+            aph ^= 1u;
+          }
+        }
+        if (ok) bar_commit(t_full + 8 * acc);
+      }
+      // all MMAs issued by this thread complete before the CTA releases TMEM
+      bar_commit(drain);
+      wait.drain(drain, 0u, DEVERR_TIMEOUT_MMA, ok ? W4_TIMEOUT_NS : W4_DRAIN_NS);
+    }
+  } else if (warp >= W4_FIRST_DQ && warp < W4_FIRST_EPI) {
+    // ---------------- dequantisers ----------------
+    const int q = warp & 3, set = (warp - W4_FIRST_DQ) >> 2;
+    // row of the stage's codes, and where its scales start and step
+    const int row = GLU ? (lane & 16) * 4 + 16 * q + (lane & 15) : 32 * q + lane;
+    const int side = GLU ? (lane & 16) * (W4_SIDE_BYTES / 32) + 16 * q + (lane & 15) : row;
+    const int pitch = GLU ? 64 : 128;
+    const int shift = p.group == 32 ? 5 : p.group == 64 ? 6 : 7;
+    const uint32_t trow = tmem_base + W4_ACC_COLS + ((uint32_t)(32 * q) << 16);
+    int wst = 0, ast = 0;
+    uint32_t wph = 0, aph = 1, turn = 0;        // turn: A stages before this one, over all tiles
+    bool ok = true;
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      for (int s = 0; s < nws && ok; ++s) {
+        if (!wait.warp(w_full + 8 * wst, wph, DEVERR_TIMEOUT_TMA, lane)) {
+          ok = false;
+          break;
+        }
+        const uint8_t* st = ws + wst * W4_W_STAGE;
+        const uint8_t* sc = st + W4_CODE_BYTES + side;
+        const uint8_t* zp = sc + W4_SIDE_BYTES;
+        const int here = min(4, nkb - 4 * s);
+        for (int b0 = 0; b0 < here; b0 += W4_KA / W4_KB, ++turn) {
+          if (turn % W4_DQ_SETS == set) {
+#pragma unroll
+            for (int h = 0; h < W4_KA / W4_KB; ++h) {
+              const int b = b0 + h;             // 64-element block of the stage
+              if (b >= here) break;
+              const uint8_t* src = st + row * 128;
+              const uint4 c0 =
+                  *reinterpret_cast<const uint4*>(src + (((2 * b) ^ (row & 7)) << 4));
+              const uint4 c1 =
+                  *reinterpret_cast<const uint4*>(src + (((2 * b + 1) ^ (row & 7)) << 4));
+              const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+              uint32_t r[32];
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {     // 32-element halves of the block
+                const int at = ((64 * b + 32 * j) >> shift) * pitch;
+                const __nv_bfloat162 s2 = __float2bfloat162_rn(w4_scale(sc[at]));
+                const uint32_t zb = 0x4300u + (p.zeros ? zp[at] : 8u);
+                const __nv_bfloat162 z2 = pair(zb | (zb << 16));
+#pragma unroll
+                for (int c = 0; c < 4; ++c) dequant_word(w[2 * c + j], z2, s2, r + 16 * j + 4 * c);
+              }
+              if (h == 0) {
+                if (!wait.warp(a_empty + 8 * ast, aph, DEVERR_TIMEOUT_EPI, lane)) {
+                  ok = false;
+                  break;
+                }
+                tc_fence_after();
+              }
+              tmem_st32(trow + ast * W4_A_COLS + h * (W4_KB / 2), r);
+            }
+            if (!ok) break;
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(a_full + 8 * ast);
+          }
+          if (++ast == W4_A_STAGES) {
+            ast = 0;
+            aph ^= 1u;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) bar_arrive(w_empty + 8 * wst);
+        if (++wst == WS) {
+          wst = 0;
+          wph ^= 1u;
+        }
+      }
+    }
+  } else if (warp >= W4_FIRST_EPI) {
+    // ---------------- epilogue ----------------
+    const int q = warp & 3, set = (warp - W4_FIRST_EPI) >> 2;
+    int g = 0, it = 0;
+    for (int t = blockIdx.x; t < total; t += gridDim.x, ++it) {
+      const W4Tile tl = w4_locate<NT>(t, grp_off, tile_pre, g);
+      const int acc = it % ACCS;
+      const int feat = tl.n_idx * FEATS + (GLU ? 16 * q + (lane & 15) : 32 * q + lane);
+      const float* rs = GLU && lane < 16 ? p.rs1 : p.rs0;
+      const float f = feat < p.N ? __ldg(rs + (int64_t)tl.g * p.N + feat) : 0.f;
+      if (!wait.warp(t_full + 8 * acc, (uint32_t)((it / ACCS) & 1), DEVERR_TIMEOUT_EPI, lane))
+        break;
+      tc_fence_after();
+      const bool rows_ok = tl.row0 >= 0 && (int64_t)tl.row0 + tl.ntok <= p.rows;
+      if (!rows_ok && lane == 0) atomicCAS(p.err, 0, DEVERR_BOUNDS);
+      const bool st = rows_ok && feat < p.N;
+      const uint32_t d = tmem_base + acc * (W4_ACC_COLS / ACCS) + ((uint32_t)(32 * q) << 16);
+      __nv_bfloat16* o = p.out + (int64_t)tl.row0 * p.N + feat;
+#pragma unroll 1
+      for (int c = 16 * set; c < tl.ntok; c += 16 * W4_EPI_SETS) {
+        uint32_t v[16];
+        tmem_ld16(d + c, v);
+        tmem_wait_ld();
+        if (GLU) {
+          // lane i and i + 16 hold gate and up of a feature: they take the even and the odd
+          // tokens of a pair
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            const float even = __uint_as_float(v[i]) * f, odd = __uint_as_float(v[i + 1]) * f;
+            const float got = __shfl_xor_sync(kFull, lane < 16 ? odd : even, 16);
+            const float gate = lane < 16 ? even : got, up = lane < 16 ? got : odd;
+            const int tok = c + i + (lane >> 4);
+            if (st && tok < tl.ntok)
+              o[(int64_t)tok * p.N] =
+                  __float2bfloat16_rn(__fdividef(gate, 1.0f + __expf(-gate)) * up);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float y = __uint_as_float(v[i]) * f;
+            if (p.act == MOE_ACT_RELU) y = y < 0.f ? 0.f : y;        // a NaN stays one
+            if (p.act == MOE_ACT_GELU) y = 0.5f * y * (1.0f + erff(y * 0.70710678118654752f));
+            if (st && c + i < tl.ntok) o[(int64_t)(c + i) * p.N] = __float2bfloat16_rn(y);
+          }
+        }
+      }
+      // every TMEM read of this tile has completed: release the accumulator
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(t_empty + 8 * acc);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                 "r"(W4_TMEM_COLS)
+                 : "memory");
+  }
+}
+
+template <int NT>
+size_t w4_smem(int G) {
+  using S = W4Shape<NT>;
+  return 1024 + (size_t)S::XS * NT * S::XK * 2 + (size_t)S::WS * W4_W_STAGE +
+         (2 * S::WS + 2 * S::XS + 2 * W4_A_STAGES + 2 * S::ACCS + 1) * 8 + 8 +
+         (size_t)2 * (G + 1) * sizeof(int);
+}
+
+struct W4Maps {
+  CUtensorMap x, c0, c1, s0, s1, z0, z1;
+};
+
+template <int NT, bool GLU>
+cudaError_t launch(const W4Maps& m, const W4Params& p, int64_t a_rows, cudaStream_t s) {
+  const size_t smem = w4_smem<NT>(p.G);
+  auto kern = w4_gemm_kernel<NT, GLU>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const int64_t most = ((a_rows + NT - 1) / NT + p.G) * (int64_t)p.nt;
+  const int sms = gemm_sm_count();
+  const int grid = (int)(most < sms ? most : sms);
+  return launch_pdl(kern, dim3(grid), dim3(W4_THREADS), smem, s, m.x, m.c0, m.c1, m.s0, m.s1, m.z0,
+                    m.z1, p);
+}
+
+}  // namespace
+
+cudaError_t launch_w4_gemm(int act, const void* a, int64_t a_rows, int K, const moe_w4_t* gate,
+                           const moe_w4_t* w, int G, int N, const int32_t* offsets, void* out,
+                           cudaStream_t s) {
+  if (a_rows <= 0 || G <= 0) return cudaSuccess;
+  const int groups = (K + w->group - 1) / w->group;
+  // tensor-map coordinates are 32-bit
+  if (a_rows > INT32_MAX || (int64_t)G * N > INT32_MAX || (int64_t)G * groups > INT32_MAX)
+    return cudaErrorInvalidValue;
+  const bool glu = gate != nullptr;
+  const int feats = glu ? 64 : 128;
+  alignas(64) W4Maps m;
+  auto maps = [&](const moe_w4_t* q, CUtensorMap* c, CUtensorMap* sc, CUtensorMap* z) {
+    const int gs = W4_KS / q->group;
+    if (!make_map_u8(c, q->codes, (uint64_t)G * N, (uint64_t)K / 2, feats, 128, true)) return false;
+    if (!make_map_u8(sc, q->scales, (uint64_t)G * groups, (uint64_t)N, gs, feats, false))
+      return false;
+    return make_map_u8(z, q->zeros ? q->zeros : q->scales, (uint64_t)G * groups, (uint64_t)N, gs,
+                       feats, false);
+  };
+  if (!make_map(&m.x, a, (uint64_t)a_rows, (uint64_t)K, W4_XBOX, W4_KB) ||
+      !maps(w, &m.c0, &m.s0, &m.z0) || !maps(glu ? gate : w, &m.c1, &m.s1, &m.z1))
+    return cudaErrorInvalidValue;
+  W4Params p{};
+  p.offsets = offsets;
+  p.rs0 = w->row_scale;
+  p.rs1 = glu ? gate->row_scale : nullptr;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.err = device_error_word();
+  p.rows = a_rows;
+  p.G = G;
+  p.N = N;
+  p.K = K;
+  p.group = w->group;
+  p.act = act;
+  p.zeros = w->zeros ? 1 : 0;
+  p.nt = (N + feats - 1) / feats;
+  p.fault = gemm_fault();
+  const int64_t mean = (a_rows + G - 1) / G;
+  if (mean > 128)
+    return glu ? launch<256, true>(m, p, a_rows, s) : launch<256, false>(m, p, a_rows, s);
+  if (mean > 24)
+    return glu ? launch<128, true>(m, p, a_rows, s) : launch<128, false>(m, p, a_rows, s);
+  return glu ? launch<32, true>(m, p, a_rows, s) : launch<32, false>(m, p, a_rows, s);
+}
+
+}  // namespace moe
