@@ -57,8 +57,11 @@ constexpr int W4_A_STAGES = 4;
 constexpr int W4_A_COLS = W4_KA / 2;
 constexpr int W4_ACC_COLS = 256;
 constexpr int W4_TMEM_COLS = 512;
-constexpr int W4_DQ_SETS = 2;
-constexpr int W4_EPI_SETS = 2;
+// A stage of the A ring belongs to one set of dequantisers: another set could be two rounds ahead of
+// it and take the wait's parity for its own.
+constexpr int W4_DQ_SETS = 4;
+static_assert(W4_A_STAGES % W4_DQ_SETS == 0, "a stage has one set of dequantisers");
+constexpr int W4_EPI_SETS = 1;
 constexpr int W4_FIRST_DQ = 4;
 constexpr int W4_FIRST_EPI = W4_FIRST_DQ + 4 * W4_DQ_SETS;
 constexpr int W4_THREADS = 32 * (W4_FIRST_EPI + 4 * W4_EPI_SETS);
@@ -106,8 +109,9 @@ __device__ __forceinline__ W4Tile w4_locate(int t, const int* grp_off, const int
   return r;
 }
 
-// Barrier steps on shared-memory addresses.  The common case of a wait, a phase that has passed,
-// is inline: through mbar_wait's call the MMA thread ran a quarter slower.
+// Barrier steps on shared-memory addresses.  Every role runs as a whole warp with one elected lane
+// issuing, and waits are inline and taken by all lanes together: no call and no divergence stands
+// between a role's loop counters and the uniform registers that its descriptors come from.
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -122,28 +126,39 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 struct W4Wait {
   volatile int* abort_flag;
   int* err;
-  // one thread
-  __device__ __forceinline__ bool one(uint32_t bar, uint32_t parity, int code) const {
-    if (bar_try(bar, parity)) return true;
-    return mbar_wait(static_cast<uint64_t*>(__cvta_shared_to_generic(bar)), parity, abort_flag,
-                     err, code, W4_TIMEOUT_NS);
-  }
-  // a whole warp: one try by all lanes, then lane 0 polls
-  __device__ __forceinline__ bool warp(uint32_t bar, uint32_t parity, int code, int lane) const {
+  // Whole warp; false when it gave up: after its time limit (which records `code` and raises the
+  // CTA's abort flag) or, with kHonor, once another role has.
+  template <bool kHonor = true>
+  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity, int code,
+                                             uint64_t limit = W4_TIMEOUT_NS) const {
     if (__all_sync(kFull, bar_try(bar, parity))) return true;
-    int ok = 1;
-    if (lane == 0)
-      ok = mbar_wait(static_cast<uint64_t*>(__cvta_shared_to_generic(bar)), parity, abort_flag,
-                     err, code, W4_TIMEOUT_NS);
-    return __shfl_sync(kFull, ok, 0) != 0;
+    const uint64_t t0 = gtimer();
+#pragma unroll 1
+    while (!__all_sync(kFull, bar_try(bar, parity))) {
+      if (kHonor && __any_sync(kFull, *abort_flag)) return false;
+      if (__any_sync(kFull, gtimer() - t0 > limit)) {
+        *abort_flag = 1;
+        atomicCAS(err, 0, code);
+        return false;
+      }
+    }
+    return true;
   }
-  // copies or MMAs in flight, before the CTA exits
+  // Copies or MMAs in flight, before the CTA exits.
   __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, int code,
                                         uint64_t limit) const {
-    mbar_wait(static_cast<uint64_t*>(__cvta_shared_to_generic(bar)), parity, abort_flag, err,
-              code, limit, /*honor_abort=*/false);
+    (void)operator()<false>(bar, parity, code, limit);
   }
 };
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -199,6 +214,13 @@ __device__ __forceinline__ uint32_t bits(__nv_bfloat162 v) {
 }
 __device__ __forceinline__ __nv_bfloat162 pair(uint32_t v) {
   return *reinterpret_cast<__nv_bfloat162*>(&v);
+}
+
+__device__ __forceinline__ __nv_bfloat162 scale_pair(uint8_t s) {
+  return __float2bfloat162_rn(w4_scale(s));
+}
+__device__ __forceinline__ __nv_bfloat162 zero_pair(uint32_t z) {     // 128 + z
+  return pair((0x4300u + z) * 0x10001u);
 }
 
 // Eight weights of a word as four bf16 pairs: (128 + code) by bits, minus (128 + zero), times
@@ -303,147 +325,150 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
   const int gs = W4_KS / p.group;               // scale rows of a weight stage
   const int groups = (p.K + p.group - 1) / p.group;
 
+  const bool leader = elect_one();              // of the warp: the lane that issues
+
   if (warp == 0) {
     // ---------------- weights ----------------
-    if (lane == 0) {
-      int stage = 0, g = 0;
-      uint32_t phase = 0, issued = 0, issued_par = 0;
-      bool ok = true;
-      // a box moves its full size, parts outside the tensor as zeros
-      const uint32_t tx = W4_CODE_BYTES + gs * W4_ROWS * (p.zeros ? 2 : 1);
-      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-        const W4Tile tl = w4_locate<NT>(t, grp_off, tile_pre, g);
-        const int n0 = tl.n_idx * FEATS, row = tl.g * p.N + n0;
-        for (int s = 0; s < nws; ++s) {
-          if (!wait.one(w_empty + 8 * stage, phase ^ 1u, DEVERR_TIMEOUT_TMA)) {
-            ok = false;
-            break;
-          }
-          const uint32_t bar = w_full + 8 * stage;
-          bar_expect(bar, tx);
-          // test hook: the stage is armed but never loaded, so the dequantisers' wait runs out
-          if (!(p.fault == 1 && blockIdx.x == 0 && t == (int)blockIdx.x && s == 0)) {
-            const uint32_t c = xs + XS * X_STAGE + stage * W4_W_STAGE, sc = c + W4_CODE_BYTES,
-                           z = sc + W4_SIDE_BYTES;
-            const int kx = s * (W4_KS / 2), ky = tl.g * groups + s * gs;
-            if (GLU) {
-              bar_load(c, &tmC1, bar, kx, row);
-              bar_load(c + W4_CODE_BYTES / 2, &tmC0, bar, kx, row);
-              bar_load(sc, &tmS1, bar, n0, ky);
-              bar_load(sc + W4_SIDE_BYTES / 2, &tmS0, bar, n0, ky);
-              if (p.zeros) {
-                bar_load(z, &tmZ1, bar, n0, ky);
-                bar_load(z + W4_SIDE_BYTES / 2, &tmZ0, bar, n0, ky);
-              }
-            } else {
-              bar_load(c, &tmC0, bar, kx, row);
-              bar_load(sc, &tmS0, bar, n0, ky);
-              if (p.zeros) bar_load(z, &tmZ0, bar, n0, ky);
+    int stage = 0, g = 0;
+    uint32_t phase = 0, issued = 0, issued_par = 0;
+    bool ok = true;
+    // a box moves its full size, parts outside the tensor as zeros
+    const uint32_t tx = W4_CODE_BYTES + gs * W4_ROWS * (p.zeros ? 2 : 1);
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const W4Tile tl = w4_locate<NT>(t, grp_off, tile_pre, g);
+      const int n0 = tl.n_idx * FEATS, row = tl.g * p.N + n0;
+      for (int s = 0; s < nws; ++s) {
+        if (!wait(w_empty + 8 * stage, phase ^ 1u, DEVERR_TIMEOUT_TMA)) {
+          ok = false;
+          break;
+        }
+        const uint32_t bar = w_full + 8 * stage;
+        // test hook: the stage is armed but never loaded, so the dequantisers' wait runs out
+        const bool load = !(p.fault == 1 && blockIdx.x == 0 && t == (int)blockIdx.x && s == 0);
+        if (leader) bar_expect(bar, tx);
+        if (leader && load) {
+          const uint32_t c = xs + XS * X_STAGE + stage * W4_W_STAGE, sc = c + W4_CODE_BYTES,
+                         z = sc + W4_SIDE_BYTES;
+          const int kx = s * (W4_KS / 2), ky = tl.g * groups + s * gs;
+          if (GLU) {
+            bar_load(c, &tmC1, bar, kx, row);
+            bar_load(c + W4_CODE_BYTES / 2, &tmC0, bar, kx, row);
+            bar_load(sc, &tmS1, bar, n0, ky);
+            bar_load(sc + W4_SIDE_BYTES / 2, &tmS0, bar, n0, ky);
+            if (p.zeros) {
+              bar_load(z, &tmZ1, bar, n0, ky);
+              bar_load(z + W4_SIDE_BYTES / 2, &tmZ0, bar, n0, ky);
             }
-            issued |= 1u << stage;
-            issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
-          }
-          if (++stage == WS) {
-            stage = 0;
-            phase ^= 1u;
+          } else {
+            bar_load(c, &tmC0, bar, kx, row);
+            bar_load(sc, &tmS0, bar, n0, ky);
+            if (p.zeros) bar_load(z, &tmZ0, bar, n0, ky);
           }
         }
+        if (load) {
+          issued |= 1u << stage;
+          issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+        }
+        if (++stage == WS) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      // the last copies land before the CTA exits, whatever became of their consumers
-      for (int s = 0; s < WS; ++s)
-        if (issued & (1u << s))
-          wait.drain(w_full + 8 * s, (issued_par >> s) & 1u, DEVERR_TIMEOUT_TMA, W4_DRAIN_NS);
     }
+    // the last copies land before the CTA exits, whatever became of their consumers
+    for (int s = 0; s < WS; ++s)
+      if (issued & (1u << s))
+        wait.drain(w_full + 8 * s, (issued_par >> s) & 1u, DEVERR_TIMEOUT_TMA, W4_DRAIN_NS);
   } else if (warp == 1) {
     // ---------------- token rows ----------------
-    if (lane == 0) {
-      int stage = 0, g = 0;
-      uint32_t phase = 0, issued = 0, issued_par = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-        const W4Tile tl = w4_locate<NT>(t, grp_off, tile_pre, g);
-        const int nbox = (tl.ntok + W4_XBOX - 1) / W4_XBOX;
-        for (int kb = 0; kb < nkb; kb += XB) {
-          if (!wait.one(x_empty + 8 * stage, phase ^ 1u, DEVERR_TIMEOUT_TMA)) {
-            ok = false;
-            break;
-          }
-          const uint32_t bar = x_full + 8 * stage;
-          const int here = min(XB, nkb - kb);
+    int stage = 0, g = 0;
+    uint32_t phase = 0, issued = 0, issued_par = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const W4Tile tl = w4_locate<NT>(t, grp_off, tile_pre, g);
+      const int nbox = (tl.ntok + W4_XBOX - 1) / W4_XBOX;
+      for (int kb = 0; kb < nkb; kb += XB) {
+        if (!wait(x_empty + 8 * stage, phase ^ 1u, DEVERR_TIMEOUT_TMA)) {
+          ok = false;
+          break;
+        }
+        const uint32_t bar = x_full + 8 * stage;
+        const int here = min(XB, nkb - kb);
+        if (leader) {
           bar_expect(bar, here * nbox * W4_XBOX_BYTES);
           for (int h = 0; h < here; ++h)
             for (int b = 0; b < nbox; ++b)
               bar_load(xs + stage * X_STAGE + h * X_BOX + b * W4_XBOX_BYTES, &tmX, bar,
                        (kb + h) * W4_KB, tl.row0 + b * W4_XBOX);
-          issued |= 1u << stage;
-          issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
-          if (++stage == XS) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        issued |= 1u << stage;
+        issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+        if (++stage == XS) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      for (int s = 0; s < XS; ++s)
-        if (issued & (1u << s))
-          wait.drain(x_full + 8 * s, (issued_par >> s) & 1u, DEVERR_TIMEOUT_TMA, W4_DRAIN_NS);
     }
+    for (int s = 0; s < XS; ++s)
+      if (issued & (1u << s))
+        wait.drain(x_full + 8 * s, (issued_par >> s) & 1u, DEVERR_TIMEOUT_TMA, W4_DRAIN_NS);
   } else if (warp == 2) {
     // ---------------- MMA issuer ----------------
-    if (lane == 0) {
-      int xst = 0, ast = 0, it = 0, g = 0;
-      uint32_t xph = 0, aph = 0;
-      bool ok = true;
-      const uint64_t bdesc = sdesc<W4_KB>(xs);
-      for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++it) {
-        const W4Tile tl = w4_locate<NT>(t, grp_off, tile_pre, g);
-        const uint32_t idesc = idesc_bf16(W4_ROWS, (tl.ntok + 15) & ~15);
-        const int acc = it % ACCS;
-        const uint32_t d = tmem_base + acc * (W4_ACC_COLS / ACCS);
-        if (!wait.one(t_empty + 8 * acc, (uint32_t)((it / ACCS) & 1) ^ 1u, DEVERR_TIMEOUT_MMA)) {
+    int xst = 0, ast = 0, it = 0, g = 0;
+    uint32_t xph = 0, aph = 0;
+    bool ok = true;
+    const uint64_t bdesc = sdesc<W4_KB>(xs);
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++it) {
+      const W4Tile tl = w4_locate<NT>(t, grp_off, tile_pre, g);
+      const uint32_t idesc =
+          idesc_bf16(W4_ROWS, __shfl_sync(kFull, (tl.ntok + 15) & ~15, 0));
+      const int acc = it % ACCS;
+      const uint32_t d = tmem_base + acc * (W4_ACC_COLS / ACCS);
+      if (!wait(t_empty + 8 * acc, (uint32_t)((it / ACCS) & 1) ^ 1u, DEVERR_TIMEOUT_MMA)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      for (int kb = 0; kb < nkb && ok; kb += W4_KA / W4_KB) {
+        if (!wait(a_full + 8 * ast, aph, DEVERR_TIMEOUT_MMA)) {
           ok = false;
           break;
         }
-        tc_fence_after();
-        for (int kb = 0; kb < nkb && ok; kb += W4_KA / W4_KB) {
-          if (!wait.one(a_full + 8 * ast, aph, DEVERR_TIMEOUT_MMA)) {
+        const uint32_t a0 = tmem_base + W4_ACC_COLS + ast * W4_A_COLS;
+#pragma unroll
+        for (int h = 0; h < W4_KA / W4_KB; ++h) {
+          if (kb + h >= nkb) break;
+          const int xb = (kb + h) % XB;         // box within the token stage
+          if (xb == 0 && !wait(x_full + 8 * xst, xph, DEVERR_TIMEOUT_MMA)) {
             ok = false;
             break;
           }
-          const uint32_t a0 = tmem_base + W4_ACC_COLS + ast * W4_A_COLS;
-#pragma unroll
-          for (int h = 0; h < W4_KA / W4_KB; ++h) {
-            if (kb + h >= nkb) break;
-            const int xb = (kb + h) % XB;       // box within the token stage
-            if (xb == 0 && !wait.one(x_full + 8 * xst, xph, DEVERR_TIMEOUT_MMA)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint64_t b = bdesc + (uint32_t)((xst * X_STAGE + xb * X_BOX) >> 4);
+          tc_fence_after();
+          const uint64_t b = bdesc + (uint32_t)((xst * X_STAGE + xb * X_BOX) >> 4);
+          const bool last = xb == XB - 1 || kb + h == nkb - 1;
+          if (leader) {
 #pragma unroll
             for (int k = 0; k < W4_KB / 16; ++k)
               umma_bf16_ts(d, a0 + h * (W4_KB / 2) + 8 * k, b + 2 * k, (kb | h | k) ? 1u : 0u,
                            idesc);
-            if (xb == XB - 1 || kb + h == nkb - 1) {
-              bar_commit(x_empty + 8 * xst);
-              if (++xst == XS) {
-                xst = 0;
-                xph ^= 1u;
-              }
-            }
+            if (last) bar_commit(x_empty + 8 * xst);
           }
-          bar_commit(a_empty + 8 * ast);
-          if (++ast == W4_A_STAGES) {
-            ast = 0;
-            aph ^= 1u;
+          if (last && ++xst == XS) {
+            xst = 0;
+            xph ^= 1u;
           }
         }
-        if (ok) bar_commit(t_full + 8 * acc);
+        if (leader) bar_commit(a_empty + 8 * ast);
+        if (++ast == W4_A_STAGES) {
+          ast = 0;
+          aph ^= 1u;
+        }
       }
-      // all MMAs issued by this thread complete before the CTA releases TMEM
-      bar_commit(drain);
-      wait.drain(drain, 0u, DEVERR_TIMEOUT_MMA, ok ? W4_TIMEOUT_NS : W4_DRAIN_NS);
+      if (ok && leader) bar_commit(t_full + 8 * acc);
     }
+    // all MMAs issued by this thread complete before the CTA releases TMEM
+    if (leader) bar_commit(drain);
+    wait.drain(drain, 0u, DEVERR_TIMEOUT_MMA, ok ? W4_TIMEOUT_NS : W4_DRAIN_NS);
   } else if (warp >= W4_FIRST_DQ && warp < W4_FIRST_EPI) {
     // ---------------- dequantisers ----------------
     const int q = warp & 3, set = (warp - W4_FIRST_DQ) >> 2;
@@ -458,7 +483,7 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     bool ok = true;
     for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
       for (int s = 0; s < nws && ok; ++s) {
-        if (!wait.warp(w_full + 8 * wst, wph, DEVERR_TIMEOUT_TMA, lane)) {
+        if (!wait(w_full + 8 * wst, wph, DEVERR_TIMEOUT_TMA)) {
           ok = false;
           break;
         }
@@ -468,28 +493,44 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         const int here = min(4, nkb - 4 * s);
         for (int b0 = 0; b0 < here; b0 += W4_KA / W4_KB, ++turn) {
           if (turn % W4_DQ_SETS == set) {
+            // everything of the A stage's 128 k first: codes, scales, zero points (a block past K
+            // is read as zeros or the next matrix's scales, and no MMA takes it)
+            const uint8_t* src = st + row * 128;
+            uint4 c[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              c[i] = *reinterpret_cast<const uint4*>(src + (((2 * b0 + i) ^ (row & 7)) << 4));
+            __nv_bfloat162 s2[4], z2[4];        // per 32 k
+            const int at = ((W4_KB * b0) >> shift) * pitch;
+            s2[0] = scale_pair(sc[at]);
+            z2[0] = zero_pair(p.zeros ? zp[at] : 8u);
+            if (shift == 7) {
+              s2[1] = s2[2] = s2[3] = s2[0];
+              z2[1] = z2[2] = z2[3] = z2[0];
+            } else if (shift == 6) {
+              s2[1] = s2[0];
+              z2[1] = z2[0];
+              s2[2] = s2[3] = scale_pair(sc[at + pitch]);
+              z2[2] = z2[3] = zero_pair(p.zeros ? zp[at + pitch] : 8u);
+            } else {
+#pragma unroll
+              for (int i = 1; i < 4; ++i) {
+                s2[i] = scale_pair(sc[at + i * pitch]);
+                z2[i] = zero_pair(p.zeros ? zp[at + i * pitch] : 8u);
+              }
+            }
 #pragma unroll
             for (int h = 0; h < W4_KA / W4_KB; ++h) {
-              const int b = b0 + h;             // 64-element block of the stage
-              if (b >= here) break;
-              const uint8_t* src = st + row * 128;
-              const uint4 c0 =
-                  *reinterpret_cast<const uint4*>(src + (((2 * b) ^ (row & 7)) << 4));
-              const uint4 c1 =
-                  *reinterpret_cast<const uint4*>(src + (((2 * b + 1) ^ (row & 7)) << 4));
-              const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+              const uint4 lo = c[2 * h], hi = c[2 * h + 1];
+              const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
               uint32_t r[32];
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {     // 32-element halves of the block
-                const int at = ((64 * b + 32 * j) >> shift) * pitch;
-                const __nv_bfloat162 s2 = __float2bfloat162_rn(w4_scale(sc[at]));
-                const uint32_t zb = 0x4300u + (p.zeros ? zp[at] : 8u);
-                const __nv_bfloat162 z2 = pair(zb | (zb << 16));
+              for (int j = 0; j < 2; ++j)       // 32-element halves of the block
 #pragma unroll
-                for (int c = 0; c < 4; ++c) dequant_word(w[2 * c + j], z2, s2, r + 16 * j + 4 * c);
-              }
+                for (int i = 0; i < 4; ++i)
+                  dequant_word(w[2 * i + j], z2[2 * h + j], s2[2 * h + j], r + 16 * j + 4 * i);
               if (h == 0) {
-                if (!wait.warp(a_empty + 8 * ast, aph, DEVERR_TIMEOUT_EPI, lane)) {
+                if (!wait(a_empty + 8 * ast, aph, DEVERR_TIMEOUT_EPI)) {
                   ok = false;
                   break;
                 }
@@ -526,7 +567,7 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
       const int feat = tl.n_idx * FEATS + (GLU ? 16 * q + (lane & 15) : 32 * q + lane);
       const float* rs = GLU && lane < 16 ? p.rs1 : p.rs0;
       const float f = feat < p.N ? __ldg(rs + (int64_t)tl.g * p.N + feat) : 0.f;
-      if (!wait.warp(t_full + 8 * acc, (uint32_t)((it / ACCS) & 1), DEVERR_TIMEOUT_EPI, lane))
+      if (!wait(t_full + 8 * acc, (uint32_t)((it / ACCS) & 1), DEVERR_TIMEOUT_EPI))
         break;
       tc_fence_after();
       const bool rows_ok = tl.row0 >= 0 && (int64_t)tl.row0 + tl.ntok <= p.rows;
