@@ -244,13 +244,15 @@ cudaError_t launch_quantize_w4(int n_matrices, int N, int K, bool bf16, const vo
                                const moe_w4_t& o, cudaStream_t s);
 cudaError_t launch_dequantize_w4(int n_matrices, int N, int K, const moe_w4_t& w, bool bf16,
                                  void* out, cudaStream_t s);
-// w4_product.cu: out[r, n] = act(sum_k a[r, k] W_g[n, k]) for the rows r of group g, or
+// 4-bit products: out[r, n] = act(sum_k a[r, k] W_g[n, k]) for the rows r of group g, or
 // SiLU(gate) * up with gate != null; act: MOE_ACT_* or -1 (none: the down projection).  bf16 a
 // [a_rows, K] and out [a_rows, N].
-cudaError_t launch_w4_product(int act, const void* a, int64_t a_rows, int K, const moe_w4_t* gate,
-                              const moe_w4_t* w, int G, int N, const int32_t* offsets, void* out,
-                              cudaStream_t s);
-
+// w4_stream.cu: the same product for few rows per group (mma.sync, weight streaming), and the
+// rows of a group that it takes at a time (0: K is too long for it)
+int w4_stream_tokens(int K, int G);
+cudaError_t launch_w4_stream(int act, const void* a, int64_t a_rows, int K, const moe_w4_t* gate,
+                             const moe_w4_t* w, int G, int N, const int32_t* offsets, void* out,
+                             cudaStream_t s);
 // w4_gemm.cu: the same product on tcgen05, for any number of rows
 cudaError_t launch_w4_gemm(int act, const void* a, int64_t a_rows, int K, const moe_w4_t* gate,
                            const moe_w4_t* w, int G, int N, const int32_t* offsets, void* out,

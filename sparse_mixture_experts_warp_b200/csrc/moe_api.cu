@@ -755,6 +755,17 @@ static moe_status_t check_w4_up(const moe_desc_t* d, const moe_w4_t* gate, const
   return MOE_OK;
 }
 
+// The streaming kernel reads the weights of a group once per P rows (P tokens fit its shared
+// memory): taken when that is at most about once per group.
+static cudaError_t launch_w4_product(int act, const void* a, int64_t a_rows, int K,
+                                     const moe_w4_t* gate, const moe_w4_t* w, int G, int N,
+                                     const int32_t* offsets, void* out, cudaStream_t s) {
+  const int64_t P = w4_stream_tokens(K, G);
+  const bool few = a_rows <= P || 2 * a_rows <= P * G;
+  return few ? launch_w4_stream(act, a, a_rows, K, gate, w, G, N, offsets, out, s)
+             : launch_w4_gemm(act, a, a_rows, K, gate, w, G, N, offsets, out, s);
+}
+
 moe_status_t moe_expert_up_w4(const moe_desc_t* d, int32_t G, int32_t F, const void* a,
                               int64_t a_rows, const int32_t* offsets, const moe_w4_t* gate,
                               const moe_w4_t* up, void* h, moe_stream_t stream) {
@@ -764,7 +775,7 @@ moe_status_t moe_expert_up_w4(const moe_desc_t* d, int32_t G, int32_t F, const v
   if (st != MOE_OK) return st;
   if (!h || !is_aligned16(h)) return MOE_ERR_INVALID_ARG;
   const bool glu = d->act == MOE_ACT_SWIGLU;
-  return cuda_status(launch_w4_gemm(d->act, a, a_rows, d->D, glu ? gate : nullptr, up, G, F,
+  return cuda_status(launch_w4_product(d->act, a, a_rows, d->D, glu ? gate : nullptr, up, G, F,
                                        offsets, h, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -777,7 +788,7 @@ moe_status_t moe_expert_down_w4(const moe_desc_t* d, int32_t G, int32_t F, const
   st = check_w4(down);
   if (st != MOE_OK) return st;
   if (!y || !is_aligned16(y)) return MOE_ERR_INVALID_ARG;
-  return cuda_status(launch_w4_gemm(-1, h, a_rows, F, nullptr, down, G, d->D, offsets, y,
+  return cuda_status(launch_w4_product(-1, h, a_rows, F, nullptr, down, G, d->D, offsets, y,
                                        reinterpret_cast<cudaStream_t>(stream)));
 }
 

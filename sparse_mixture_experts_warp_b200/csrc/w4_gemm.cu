@@ -40,6 +40,7 @@
 #include "mbar.cuh"
 #include "tc_ops.cuh"
 #include "w4.cuh"
+#include "w4_wait.cuh"
 
 namespace moe {
 namespace {
@@ -65,9 +66,6 @@ constexpr int W4_EPI_SETS = 1;
 constexpr int W4_FIRST_DQ = 4;
 constexpr int W4_FIRST_EPI = W4_FIRST_DQ + 4 * W4_DQ_SETS;
 constexpr int W4_THREADS = 32 * (W4_FIRST_EPI + 4 * W4_EPI_SETS);
-constexpr uint64_t W4_TIMEOUT_NS = 2000000000ull;   // 2 s per wait
-constexpr uint64_t W4_DRAIN_NS = 200000000ull;      // 0.2 s to drain after an abort
-constexpr unsigned kFull = 0xffffffffu;
 
 // Tokens of a tile, weight stages, token stages and their k, accumulators.
 template <int NT> struct W4Shape;
@@ -107,73 +105,6 @@ __device__ __forceinline__ W4Tile w4_locate(int t, const int* grp_off, const int
   r.ntok = min(NT, m - j * NT);
   r.row0 = grp_off[g] + j * NT;
   return r;
-}
-
-// Barrier steps on shared-memory addresses.  Every role runs as a whole warp with one elected lane
-// issuing, and waits are inline and taken by all lanes together: no call and no divergence stands
-// between a role's loop counters and the uniform registers that its descriptors come from.
-__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-struct W4Wait {
-  volatile int* abort_flag;
-  int* err;
-  // Whole warp; false when it gave up: after its time limit (which records `code` and raises the
-  // CTA's abort flag) or, with kHonor, once another role has.
-  template <bool kHonor = true>
-  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity, int code,
-                                             uint64_t limit = W4_TIMEOUT_NS) const {
-    if (__all_sync(kFull, bar_try(bar, parity))) return true;
-    const uint64_t t0 = gtimer();
-#pragma unroll 1
-    while (!__all_sync(kFull, bar_try(bar, parity))) {
-      if (kHonor && __any_sync(kFull, *abort_flag)) return false;
-      if (__any_sync(kFull, gtimer() - t0 > limit)) {
-        *abort_flag = 1;
-        atomicCAS(err, 0, code);
-        return false;
-      }
-    }
-    return true;
-  }
-  // Copies or MMAs in flight, before the CTA exits.
-  __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, int code,
-                                        uint64_t limit) const {
-    (void)operator()<false>(bar, parity, code, limit);
-  }
-};
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r));
-  return r != 0;
-}
-__device__ __forceinline__ void bar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void bar_commit(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void bar_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
-                                         int y) {
-  tma_load_2d(dst, map, static_cast<uint64_t*>(__cvta_shared_to_generic(bar)), x, y);
 }
 
 __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
@@ -260,7 +191,7 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
   const uint32_t a_full = x_empty + 8 * XS, a_empty = a_full + 8 * W4_A_STAGES;
   const uint32_t t_full = a_empty + 8 * W4_A_STAGES, t_empty = t_full + 8 * ACCS;
   const uint32_t drain = t_empty + 8 * ACCS;
-  const W4Wait wait{abort_flag, p.err};
+  const BarWait wait{abort_flag, p.err};
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -308,17 +239,19 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
       int inc = tiles;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(kFull, inc, o);
+        const int v = __shfl_up_sync(kFullWarp, inc, o);
         if (lane >= o) inc += v;
       }
       if (g < p.G) tile_pre[g + 1] = carry + inc;
-      carry += __shfl_sync(kFull, inc, 31);
+      carry += __shfl_sync(kFullWarp, inc, 31);
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_holder;
+  // the CTA holds all 512 columns, so they start at 0: a constant keeps the MMA's addresses in
+  // uniform registers
+  constexpr uint32_t tmem_base = 0;
   const int total = tile_pre[p.G];
   const int nkb = p.K / W4_KB;                  // 64-element k-blocks
   const int nws = (nkb + 3) / 4;
@@ -378,7 +311,7 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     // the last copies land before the CTA exits, whatever became of their consumers
     for (int s = 0; s < WS; ++s)
       if (issued & (1u << s))
-        wait.drain(w_full + 8 * s, (issued_par >> s) & 1u, DEVERR_TIMEOUT_TMA, W4_DRAIN_NS);
+        wait.drain(w_full + 8 * s, (issued_par >> s) & 1u, DEVERR_TIMEOUT_TMA, kDrainNs);
   } else if (warp == 1) {
     // ---------------- token rows ----------------
     int stage = 0, g = 0;
@@ -411,7 +344,7 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     }
     for (int s = 0; s < XS; ++s)
       if (issued & (1u << s))
-        wait.drain(x_full + 8 * s, (issued_par >> s) & 1u, DEVERR_TIMEOUT_TMA, W4_DRAIN_NS);
+        wait.drain(x_full + 8 * s, (issued_par >> s) & 1u, DEVERR_TIMEOUT_TMA, kDrainNs);
   } else if (warp == 2) {
     // ---------------- MMA issuer ----------------
     int xst = 0, ast = 0, it = 0, g = 0;
@@ -421,7 +354,7 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++it) {
       const W4Tile tl = w4_locate<NT>(t, grp_off, tile_pre, g);
       const uint32_t idesc =
-          idesc_bf16(W4_ROWS, __shfl_sync(kFull, (tl.ntok + 15) & ~15, 0));
+          idesc_bf16(W4_ROWS, __shfl_sync(kFullWarp, (tl.ntok + 15) & ~15, 0));
       const int acc = it % ACCS;
       const uint32_t d = tmem_base + acc * (W4_ACC_COLS / ACCS);
       if (!wait(t_empty + 8 * acc, (uint32_t)((it / ACCS) & 1) ^ 1u, DEVERR_TIMEOUT_MMA)) {
@@ -468,7 +401,7 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     }
     // all MMAs issued by this thread complete before the CTA releases TMEM
     if (leader) bar_commit(drain);
-    wait.drain(drain, 0u, DEVERR_TIMEOUT_MMA, ok ? W4_TIMEOUT_NS : W4_DRAIN_NS);
+    wait.drain(drain, 0u, DEVERR_TIMEOUT_MMA, ok ? kWaitNs : kDrainNs);
   } else if (warp >= W4_FIRST_DQ && warp < W4_FIRST_EPI) {
     // ---------------- dequantisers ----------------
     const int q = warp & 3, set = (warp - W4_FIRST_DQ) >> 2;
@@ -586,7 +519,7 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
             const float even = __uint_as_float(v[i]) * f, odd = __uint_as_float(v[i + 1]) * f;
-            const float got = __shfl_xor_sync(kFull, lane < 16 ? odd : even, 16);
+            const float got = __shfl_xor_sync(kFullWarp, lane < 16 ? odd : even, 16);
             const float gate = lane < 16 ? even : got, up = lane < 16 ? got : odd;
             const int tok = c + i + (lane >> 4);
             if (st && tok < tl.ntok)
