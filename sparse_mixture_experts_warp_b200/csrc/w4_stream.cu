@@ -6,20 +6,27 @@
 // Transformer 理解 Router、Top-K 与负载均衡" (f3dlife), section 3.
 //
 // out[r, n] = epi(row_scale[n] * sum_groups scale * sum_k (code - zero) a[r, k]).  The time is the
-// codes' bytes, and next to them the integer work of unpacking: 3 shifts and 4 mask-and-or steps
-// per 8 codes (half rate on sm_100a).  So the weights go from shared memory straight into mma
-// fragments as the whole numbers code - zero (exact in bf16), and the scale multiplies the fp32
-// sum of its group of k (one step per 32..128 k instead of one per weight).
+// codes' bytes, and next to them the integer work of unpacking (half rate on sm_100a).  So
+//   - the weights go from shared memory straight into mma fragments as the whole numbers
+//     code - zero, and the scale multiplies the fp32 sum of its group of k (one step per 32..128
+//     k instead of one per weight);
+//   - the product runs in fp16, whose 10 mantissa bits take a nibble at bits 0..3 or 4..7 of a
+//     half word: one shift and four mask-and-or steps per 8 codes (bf16's 7 bits need three
+//     shifts).  A token row is scaled by the power of two that brings its largest element to
+//     [2^14, 2^15): its bf16 elements are then fp16 numbers exactly down to 2^-32 of the largest,
+//     and what lies below is off by less than 2^-40 of it, far under the fp32 sums' own rounding.
+//     The inverse power multiplies the finished sum.
 //
-// A CTA of 16 warps takes a tile of RT * 16 weight rows (SwiGLU: RT * 8 features, 8 rows of
-// W_gate above the same 8 of W_up in one m16n8k16 fragment) by up to P <= 8 tokens of a group:
-// RT warps side by side, WK = 16 / RT along K.  Every warp streams its own 16 rows x 256 k stages
-// through a private ring (TMA for the codes, 8-byte cp.async for scales and zero points), so
-// nothing but the sum over the WK warps, once a tile through shared memory, waits for another
-// warp, and the ring runs on into the next tile meanwhile.  CTAs own contiguous ranges of tiles
-// (group by group, token tiles, then weight rows), so the P token rows are copied to shared
-// memory about once per group.
+// A CTA takes a tile of RT * 16 weight rows (SwiGLU: RT * 8 features, 8 rows of W_gate above the
+// same 8 of W_up in one m16n8k16 fragment) by up to P <= 8 tokens of a group with 16 warps: RT
+// side by side, WK = 16 / RT along K.  One more warp streams 256 k per warp and stage (TMA: codes,
+// scales, zero points) into a ring that runs on from tile to tile; a warp that issued the copies
+// of its own rows between its products spent half of its instructions on that.  The warps along K
+// meet once a tile, where their partial sums go through shared memory.  CTAs own contiguous
+// ranges of tiles (group by group, token tiles, then weight rows), so the P token rows are copied
+// to shared memory about once per group.
 #include <cuda.h>
+#include <cuda_fp16.h>
 
 #include "common.cuh"
 #include "mbar.cuh"
@@ -30,17 +37,18 @@
 namespace moe {
 namespace {
 
-constexpr int ST_WARPS = 16;
-constexpr int ST_THREADS = 32 * ST_WARPS;
-constexpr int ST_K = 256;                       // k of a stage
+constexpr int ST_WARPS = 16;                    // that compute
+constexpr int ST_THREADS = 32 * (ST_WARPS + 1);
+constexpr int ST_K = 256;                       // k of a stage, per warp
 constexpr int ST_STAGES = 3;
-constexpr int ST_CODES = 16 * ST_K / 2;         // bytes of codes of a stage: 16 rows x 128
-constexpr int ST_SIDE = 128;                    // scales (or zero points): up to 8 groups x 16 rows
+constexpr int ST_CODES = ST_WARPS * 16 * ST_K / 2;          // bytes of codes of a stage
+constexpr int ST_SIDE = 2048;                   // its scales (or zero points)
+constexpr int ST_STAGE = ST_CODES + 2 * ST_SIDE;
 constexpr int ST_TOK = 8;
 constexpr int ST_PART = 16 * ST_TOK;            // fp32 partial sums of a warp
 constexpr int ST_XPAD = 64;                     // bytes: rows of x start 64 bytes apart mod 128
-constexpr size_t ST_FIXED = 1024 + (size_t)ST_WARPS * ST_STAGES * (ST_CODES + 2 * ST_SIDE + 8) +
-                            2 * ST_WARPS * ST_PART * 4 + 16;
+constexpr size_t ST_FIXED = 1024 + (size_t)ST_STAGES * ST_STAGE + 2 * ST_WARPS * ST_PART * 4 +
+                            2 * ST_STAGES * 8 + 16 + 4 * ST_TOK * 4;
 constexpr size_t ST_SMEM = 227 * 1024;
 
 struct StreamParams {
@@ -53,6 +61,7 @@ struct StreamParams {
   int G, N, K, act;
   int P;                                        // tokens per tile
   int RT, WK;
+  int side_step;                                // bytes of a scale box, rounded up to 128
   int fault;                                    // test hook: the first stage of CTA 0 never comes
 };
 
@@ -82,59 +91,101 @@ struct StreamTile {
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                           uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+// d = a b
+__device__ __forceinline__ void mma_16816_first(float (&d)[4], const uint32_t (&a)[4],
+                                                uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
-// Arrives on bar once this thread's cp.async copies so far have landed.
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+// The warps that compute, without the producer.
+__device__ __forceinline__ void sync_compute() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * ST_WARPS) : "memory");
 }
 
-// Four pairs code - zero of a word (z2 = 128 + zero twice).
-__device__ __forceinline__ void unpack_word(uint32_t w, __nv_bfloat162 z2, uint32_t (&r)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t p = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&p), z2);
-    r[i] = *reinterpret_cast<const uint32_t*>(&d);
-  }
+__device__ __forceinline__ uint32_t bits(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
+__device__ __forceinline__ __half2 halves(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
+
+// (w & mask) | 0x64006400: 1024 + nibble (mask 0x000f000f) or 1024 + 16 * nibble (0x00f000f0)
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t nibbles(uint32_t w) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "n"(MASK), "r"(0x64006400u));
+  return r;
 }
-__device__ __forceinline__ __nv_bfloat162 zero2(uint32_t z) {
-  uint32_t v = (0x4300u + z) * 0x10001u;
-  return *reinterpret_cast<__nv_bfloat162*>(&v);
+// zero points of a row as the two forms' subtrahends
+struct Zero {
+  __half2 lo, hi;                               // 1024 + zero, -(64 + zero)
+  __device__ __forceinline__ explicit Zero(uint32_t z)
+      : lo(halves((0x6400u + z) * 0x10001u)), hi(halves(((0xd400u + 16u * z)) * 0x10001u)) {}
+};
+// Four pairs code - zero of a word, exact
+__device__ __forceinline__ void unpack_word(uint32_t w, const Zero& z, uint32_t (&r)[4]) {
+  const __half2 sixteenth = halves(0x2c002c00u);
+  const uint32_t t = w >> 8;
+  r[0] = bits(__hsub2(halves(nibbles<0x000f000fu>(w)), z.lo));
+  r[1] = bits(__hfma2(halves(nibbles<0x00f000f0u>(w)), sixteenth, z.hi));
+  r[2] = bits(__hsub2(halves(nibbles<0x000f000fu>(t)), z.lo));
+  r[3] = bits(__hfma2(halves(nibbles<0x00f000f0u>(t)), sixteenth, z.hi));
+}
+// two e4m3 bytes as floats
+__device__ __forceinline__ float2 scale_two(uint32_t a, uint32_t b) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(a + 256u * b), __NV_E4M3);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// a bf16 in the low half of `v`, times p, as fp16 bits
+__device__ __forceinline__ uint32_t to_half2(uint32_t v, float p) {
+  const __half2 h = __floats2half2_rn(__uint_as_float(v << 16) * p,
+                                      __uint_as_float(v & 0xffff0000u) * p);
+  return bits(h);
 }
 
 template <bool GLU, bool ZEROS, int GROUP>
 __global__ void __launch_bounds__(ST_THREADS, 1)
 w4_stream_kernel(const __grid_constant__ CUtensorMap tmC0,
-                 const __grid_constant__ CUtensorMap tmC1, const StreamParams p) {
+                 const __grid_constant__ CUtensorMap tmC1,
+                 const __grid_constant__ CUtensorMap tmS0,
+                 const __grid_constant__ CUtensorMap tmS1,
+                 const __grid_constant__ CUtensorMap tmZ0,
+                 const __grid_constant__ CUtensorMap tmZ1, const StreamParams p) {
   constexpr int GS = ST_K / GROUP;              // scale groups of a stage
+  constexpr int MATS = GLU ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint8_t* codes = smem + warp * (ST_STAGES * ST_CODES);
-  uint8_t* side = smem + ST_WARPS * ST_STAGES * ST_CODES + warp * (ST_STAGES * 2 * ST_SIDE);
-  float* part = reinterpret_cast<float*>(smem + ST_WARPS * ST_STAGES * (ST_CODES + 2 * ST_SIDE));
+  float* part = reinterpret_cast<float*>(smem + ST_STAGES * ST_STAGE);
   uint64_t* bars = reinterpret_cast<uint64_t*>(part + 2 * ST_WARPS * ST_PART);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + ST_WARPS * ST_STAGES);
-  uint8_t* xs = reinterpret_cast<uint8_t*>(bars + ST_WARPS * ST_STAGES) + 16;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 2 * ST_STAGES);
+  float* back = reinterpret_cast<float*>(bars + 2 * ST_STAGES) + 4;          // [2][ST_TOK]: the
+                                                // tokens' inverse powers, by parity of x loads
+  uint32_t* tops = reinterpret_cast<uint32_t*>(back + 2 * ST_TOK);           // [2][ST_TOK]: their
+                                                // largest magnitudes
+  uint8_t* xs = reinterpret_cast<uint8_t*>(tops + 2 * ST_TOK);
   const int xpitch = 2 * p.K + ST_XPAD;
   int* grp_off = reinterpret_cast<int*>(xs + p.P * xpitch);       // [G + 1]
   int* tile_pre = grp_off + (p.G + 1);                            // [G + 1]
-  const uint32_t full = smem_u32(bars + warp * ST_STAGES);
+  const uint32_t full = smem_u32(bars), empty = full + 8 * ST_STAGES;
   const BarWait wait{abort_flag, p.err};
 
-  const int feats = (GLU ? 8 : 16) * p.RT;
+  const int rows = (GLU ? 8 : 16) * p.RT;       // of a matrix in a tile: the tile's features
+  const int feats = rows;
+  const int feats_log = 31 - __clz(feats);      // RT is a power of two
   const int nt = (p.N + feats - 1) / feats;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < ST_WARPS * ST_STAGES; ++i) mbar_init(bars + i, 33);
+    for (int i = 0; i < ST_STAGES; ++i) {
+      mbar_init(bars + i, 1);
+      mbar_init(bars + ST_STAGES + i, ST_WARPS);
+    }
     *abort_flag = 0;
+    for (int i = 0; i < 2 * ST_TOK; ++i) tops[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -171,101 +222,148 @@ w4_stream_kernel(const __grid_constant__ CUtensorMap tmC0,
   const int t_lo = (int)((int64_t)total * blockIdx.x / gridDim.x);
   const int t_hi = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
   const int nst = (p.K + ST_K - 1) / ST_K;
-  const int groups = (p.K + GROUP - 1) / GROUP;
-  const int wk = warp % p.WK, rt = warp / p.WK;
   const bool leader = elect_one();
+  if (t_lo >= t_hi) return;                     // the whole CTA
+  StreamTile tl{};
+  tl.start(t_lo, grp_off, tile_pre, nt, p.P, feats);
+
+  if (warp == ST_WARPS) {
+    // ---------------- producer ----------------
+    const int groups = (p.K + GROUP - 1) / GROUP;
+    int slot = 0;
+    uint32_t phase = 0, issued = 0, issued_par = 0;
+    bool ok = true;
+    for (int t = t_lo; t < t_hi && ok; ++t) {
+      const int row = tl.g * p.N + tl.n0;
+      for (int s0 = 0; s0 < nst; s0 += p.WK) {
+        if (!wait(empty + 8 * slot, phase ^ 1u, DEVERR_TIMEOUT_TMA)) {
+          ok = false;
+          break;
+        }
+        const uint32_t bar = full + 8 * slot;
+        const int n = min(p.WK, nst - s0);      // warps along K that have a stage
+        // test hook: armed but never loaded, so the computing warps' wait runs out
+        const bool load = !(p.fault == 1 && blockIdx.x == 0 && t == t_lo && s0 == 0);
+        if (leader) {
+          bar_expect(bar, n * MATS * rows * (ST_K / 2 + GS * (ZEROS ? 2 : 1)));
+          if (load) {
+            uint32_t c = smem_u32(smem + slot * ST_STAGE), sc = c + ST_CODES;
+            for (int w = 0; w < n; ++w) {
+              const int x = (s0 + w) * (ST_K / 2), y = tl.g * groups + (s0 + w) * GS;
+              if (GLU) {
+                bar_load(c, &tmC1, bar, x, row);
+                bar_load(sc, &tmS1, bar, tl.n0, y);
+                if (ZEROS) bar_load(sc + ST_SIDE, &tmZ1, bar, tl.n0, y);
+                c += rows * 128;
+                sc += p.side_step;
+              }
+              bar_load(c, &tmC0, bar, x, row);
+              bar_load(sc, &tmS0, bar, tl.n0, y);
+              if (ZEROS) bar_load(sc + ST_SIDE, &tmZ0, bar, tl.n0, y);
+              c += rows * 128;
+              sc += p.side_step;
+            }
+          }
+        }
+        if (load) {
+          issued |= 1u << slot;
+          issued_par = (issued_par & ~(1u << slot)) | (phase << slot);
+        }
+        if (++slot == ST_STAGES) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      }
+      if (t + 1 < t_hi) tl.next(grp_off, p.N, p.P, feats);
+    }
+    // the last copies land before the CTA exits, whatever became of their consumers
+    for (int i = 0; i < ST_STAGES; ++i)
+      if (issued & (1u << i))
+        wait.drain(full + 8 * i, (issued_par >> i) & 1u, DEVERR_TIMEOUT_TMA, kDrainNs);
+    return;
+  }
+
+  // ---------------- products ----------------
+  const int wk = warp % p.WK, rt = warp / p.WK;
   const int q = lane >> 2, c = lane & 3;        // fragment row / token, and column pair
   const int prow = ((q & 3) << 1) | (q >> 2);   // weight row of fragment row q: reads of the
                                                 // swizzled rows are then free of bank conflicts
-  // ---- this warp's stream: stages wk, wk + WK, .. of every tile ----
-  StreamTile pl{};                              // tile and stage of the next request
-  int pt = wk < nst ? t_lo : t_hi, ps = wk, slot = 0;
-  if (pt < t_hi) pl.start(pt, grp_off, tile_pre, nt, p.P, feats);
-  uint32_t issued = 0, par = 0;                 // per slot: under way; parity of its phase
+  // this lane's bytes of a stage: 16-byte piece 0 of its two rows, and their scales
+  const int code0 = wk * p.RT * 2048 + rt * (GLU ? 1024 : 2048) + prow * 128 + 8 * (c & 1);
+  const int code_up = GLU ? rows * 128 : 1024;
+  const int side0 = ST_CODES + wk * MATS * p.side_step + rt * (GLU ? 8 : 16) + prow;
+  const int side_up = GLU ? p.side_step : 8;
+  const int lane_at = ((c >> 1) ^ prow) << 4;
+  int slot = 0, x_row = -1, xbuf = 0, buf = 0;
+  uint32_t phase = 0;
   bool alive = true;
-  // lane: 8 rows of a scale group, first or second half of the fragment's rows
-  const int kg = lane >> 1, half = lane & 1;
-  const uint8_t* scales = GLU && half == 0 ? p.gate.scales : p.w.scales;
-  const uint8_t* zeros = GLU && half == 0 ? p.gate.zeros : p.w.zeros;
-  const uint32_t side_dst = smem_u32(side) + 16 * kg + 8 * half;
-  auto request = [&]() {                        // into `slot`, which the warp has read
-    if (pt >= t_hi) return;
-    const int n0 = pl.n0 + rt * (GLU ? 8 : 16);
-    const uint32_t bar = full + 8 * slot;
-    const bool load = !(p.fault == 1 && blockIdx.x == 0 && warp == 0 && pt == t_lo && ps == wk);
-    if (leader) {
-      bar_expect(bar, ST_CODES);
-      if (load) {
-        const uint32_t dst = smem_u32(codes + slot * ST_CODES);
-        const int x = ps * (ST_K / 2), y = pl.g * p.N + n0;
-        if (GLU) {
-          bar_load(dst, &tmC1, bar, x, y);
-          bar_load(dst + ST_CODES / 2, &tmC0, bar, x, y);
-        } else {
-          bar_load(dst, &tmC0, bar, x, y);
-        }
-      }
-    }
-    const int at = ps * GS + kg, n = GLU ? n0 : n0 + 8 * half;
-    if (kg < GS && at < groups && n < p.N) {
-      const int64_t src = (int64_t)(pl.g * groups + at) * p.N + n;
-      cp_async8(side_dst + slot * 2 * ST_SIDE, scales + src);
-      if (ZEROS) cp_async8(side_dst + slot * 2 * ST_SIDE + ST_SIDE, zeros + src);
-    }
-    cp_async_arrive(bar);
-    if (load) issued |= 1u << slot;
-    ps += p.WK;
-    if (ps >= nst) {
-      ps = wk;
-      if (++pt < t_hi) pl.next(grp_off, p.N, p.P, feats);
-    }
-  };
-  for (slot = 0; slot < ST_STAGES; ++slot) request();
-  slot = 0;
-
-  StreamTile tl{};
-  if (t_lo < t_hi) tl.start(t_lo, grp_off, tile_pre, nt, p.P, feats);
-  int x_row = -1, buf = 0;
-  const int lane_at = ((c >> 1) ^ prow) << 4;   // 16-byte piece of block 0, swizzled
   for (int t = t_lo; t < t_hi; ++t, buf ^= 1) {
     const bool rows_ok = tl.row0 >= 0 && (int64_t)tl.row0 + tl.ntok <= p.rows;
     if (tl.row0 != x_row) {
       // token rows of the new group or token tile (every warp has read the old ones: it has
-      // arrived at the last tile's barrier)
+      // arrived at the last tile's barrier): as they are, with the largest magnitude of each,
+      // then scaled to fp16 in place, every vector by the thread that brought it
       if (!rows_ok && threadIdx.x == 0) atomicCAS(p.err, 0, DEVERR_BOUNDS);
+      xbuf ^= 1;
       const int vec = p.K / 8;
+      const uint4* src = reinterpret_cast<const uint4*>(p.a + (int64_t)tl.row0 * p.K);
+#pragma unroll 1
       for (int r = 0; r < tl.ntok; ++r) {
-        const uint4* src =
-            reinterpret_cast<const uint4*>(p.a + ((int64_t)tl.row0 + r) * p.K);
-        for (int v = threadIdx.x; v < vec; v += ST_THREADS)
-          *reinterpret_cast<uint4*>(xs + r * xpitch + 16 * v) =
-              rows_ok ? __ldg(src + v) : make_uint4(0u, 0u, 0u, 0u);
+        uint32_t top = 0;                       // as bits of a float
+#pragma unroll 4
+        for (int v = threadIdx.x; v < vec; v += 32 * ST_WARPS) {
+          const uint4 u = rows_ok ? __ldg(src + (int64_t)r * vec + v) : make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(xs + r * xpitch + 16 * v) = u;
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            top = max(top, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
+        }
+        top = __reduce_max_sync(kFullWarp, top);
+        if (lane == 0) atomicMax(&tops[xbuf * ST_TOK + r], top);
       }
-      __syncthreads();
+      sync_compute();
+#pragma unroll 1
+      for (int r = 0; r < tl.ntok; ++r) {
+        // 2^(141 - e) brings 2^(e - 127) to 2^14; infinities and NaN stay what they are
+        const int e = min(max((int)(tops[xbuf * ST_TOK + r] >> 23), 15), 254);
+        const float up = __uint_as_float((uint32_t)(268 - e) << 23);
+        for (int v = threadIdx.x; v < vec; v += 32 * ST_WARPS) {
+          uint4* at = reinterpret_cast<uint4*>(xs + r * xpitch + 16 * v);
+          const uint4 u = *at;
+          *at = make_uint4(to_half2(u.x, up), to_half2(u.y, up), to_half2(u.z, up),
+                           to_half2(u.w, up));
+        }
+        if (threadIdx.x == 0) back[xbuf * ST_TOK + r] = 1.0f / up;
+      }
+      // the other buffer's, for the next load: its readers were before the barrier above
+      if (threadIdx.x < ST_TOK) tops[(xbuf ^ 1) * ST_TOK + threadIdx.x] = 0;
+      sync_compute();
       x_row = tl.row0;
     }
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     // lanes without a token repeat the last one: their columns of the product are not used
     const uint8_t* xrow = xs + min(q, tl.ntok - 1) * xpitch + 16 * c;
-    for (int s = wk; s < nst; s += p.WK) {
-      if (alive) alive = wait(full + 8 * slot, (par >> slot) & 1u, DEVERR_TIMEOUT_TMA);
-      if (alive) {
-        const uint8_t* st = codes + slot * ST_CODES + prow * 128 + 8 * (c & 1);
-        const uint8_t* sd = side + slot * 2 * ST_SIDE + prow;
+    for (int s = wk; s < nst + wk; s += p.WK) {
+      if (alive) alive = wait(full + 8 * slot, phase, DEVERR_TIMEOUT_TMA);
+      if (alive && s < nst) {
+        const uint8_t* st = smem + slot * ST_STAGE + code0;
+        const uint8_t* sd = smem + slot * ST_STAGE + side0;
         const uint8_t* xp = xrow + s * (2 * ST_K);
         const int here = (p.K - s * ST_K) / W4_BLOCK;       // 64-element blocks of the stage
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        __nv_bfloat162 z0 = zero2(8u), z1 = zero2(8u);
+        float sum[4];
+        Zero z0(8u), z1(8u);
         auto block = [&](int b, bool last) {
           const int at = lane_at ^ (b << 5);
           const uint2 wa = *reinterpret_cast<const uint2*>(st + at);
-          const uint2 wb = *reinterpret_cast<const uint2*>(st + ST_CODES / 2 + at);
+          const uint2 wb = *reinterpret_cast<const uint2*>(st + code_up + at);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {         // 32-element halves
             const int k = 64 * b + 32 * j;
+            const uint8_t* side = sd + k / GROUP * rows;
             if (ZEROS && k % GROUP == 0) {
-              z0 = zero2(sd[ST_SIDE + 16 * (k / GROUP)]);
-              z1 = zero2(sd[ST_SIDE + 16 * (k / GROUP) + 8]);
+              z0 = Zero(side[ST_SIDE]);
+              z1 = Zero(side[ST_SIDE + side_up]);
             }
             const uint4 x = *reinterpret_cast<const uint4*>(xp + 2 * k);
             uint32_t ra[4], rb[4];
@@ -273,16 +371,17 @@ w4_stream_kernel(const __grid_constant__ CUtensorMap tmC0,
             unpack_word(j ? wb.y : wb.x, z1, rb);
             const uint32_t a0[4] = {ra[0], rb[0], ra[1], rb[1]};
             const uint32_t a1[4] = {ra[2], rb[2], ra[3], rb[3]};
-            mma_16816(sum, a0, x.x, x.y);
+            if (k % GROUP == 0)
+              mma_16816_first(sum, a0, x.x, x.y);
+            else
+              mma_16816(sum, a0, x.x, x.y);
             mma_16816(sum, a1, x.z, x.w);
             if ((k + 32) % GROUP == 0 || (j == 1 && last)) {
-              const float s0 = w4_scale(sd[16 * (k / GROUP)]);
-              const float s1 = w4_scale(sd[16 * (k / GROUP) + 8]);
-              acc[0] = fmaf(s0, sum[0], acc[0]);
-              acc[1] = fmaf(s0, sum[1], acc[1]);
-              acc[2] = fmaf(s1, sum[2], acc[2]);
-              acc[3] = fmaf(s1, sum[3], acc[3]);
-              sum[0] = sum[1] = sum[2] = sum[3] = 0.f;
+              const float2 sc = scale_two(side[0], side[side_up]);
+              acc[0] = fmaf(sc.x, sum[0], acc[0]);
+              acc[1] = fmaf(sc.x, sum[1], acc[1]);
+              acc[2] = fmaf(sc.y, sum[2], acc[2]);
+              acc[3] = fmaf(sc.y, sum[3], acc[3]);
             }
           }
         };
@@ -293,22 +392,23 @@ w4_stream_kernel(const __grid_constant__ CUtensorMap tmC0,
 #pragma unroll 1
           for (int b = 0; b < here; ++b) block(b, b == here - 1);
         }
-        __syncwarp();
-        par ^= 1u << slot;
-        issued &= ~(1u << slot);
-        request();
       }
-      if (++slot == ST_STAGES) slot = 0;
+      __syncwarp();
+      if (leader) bar_arrive(empty + 8 * slot);
+      if (++slot == ST_STAGES) {
+        slot = 0;
+        phase ^= 1u;
+      }
     }
     // sum over the WK warps of a row tile
     float* mypart = part + (buf * ST_WARPS + warp) * ST_PART + prow * ST_TOK + 2 * c;
     *reinterpret_cast<float2*>(mypart) = make_float2(acc[0], acc[1]);
     *reinterpret_cast<float2*>(mypart + 8 * ST_TOK) = make_float2(acc[2], acc[3]);
-    __syncthreads();
+    sync_compute();
     if (rows_ok) {
       constexpr int per = GLU ? 8 : 16;
-      for (int i = threadIdx.x; i < tl.ntok * feats; i += ST_THREADS) {
-        const int tok = i / feats, f = i - tok * feats;
+      for (int i = threadIdx.x; i < tl.ntok * feats; i += 32 * ST_WARPS) {
+        const int tok = i >> feats_log, f = i & (feats - 1);
         const float* src =
             part + (buf * ST_WARPS + (f / per) * p.WK) * ST_PART + (f % per) * ST_TOK + tok;
         const int n = tl.n0 + f;
@@ -319,6 +419,9 @@ w4_stream_kernel(const __grid_constant__ CUtensorMap tmC0,
           if (GLU) u += src[w * ST_PART + 8 * ST_TOK];
         }
         const int64_t nr = (int64_t)tl.g * p.N + n;
+        const float bk = back[xbuf * ST_TOK + tok];
+        v *= bk;
+        if (GLU) u *= bk;
         if (GLU) {
           v *= __ldg(p.gate.row_scale + nr);
           u *= __ldg(p.w.row_scale + nr);
@@ -333,12 +436,6 @@ w4_stream_kernel(const __grid_constant__ CUtensorMap tmC0,
     }
     if (t + 1 < t_hi) tl.next(grp_off, p.N, p.P, feats);
   }
-  // copies in flight land before the CTA exits (only after a wait that gave up)
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  if (!alive)
-    for (int s = 0; s < ST_STAGES; ++s)
-      if (issued & (1u << s))
-        wait.drain(full + 8 * s, (par >> s) & 1u, DEVERR_TIMEOUT_TMA, kDrainNs);
 }
 
 }  // namespace
@@ -360,11 +457,6 @@ cudaError_t launch_w4_stream(int act, const void* a, int64_t a_rows, int K, cons
   p.P = w4_stream_tokens(K, G);
   if (p.P < 1 || (int64_t)G * N > INT32_MAX) return cudaErrorInvalidValue;
   if (a_rows < p.P) p.P = (int)a_rows;
-  alignas(64) CUtensorMap c0, c1;
-  if (!make_map_u8(&c0, w->codes, (uint64_t)G * N, (uint64_t)K / 2, glu ? 8 : 16, 128, true) ||
-      !make_map_u8(&c1, glu ? gate->codes : w->codes, (uint64_t)G * N, (uint64_t)K / 2,
-                   glu ? 8 : 16, 128, true))
-    return cudaErrorInvalidValue;
   auto ptrs = [](const moe_w4_t* q) {
     return W4Ptrs{reinterpret_cast<const uint32_t*>(q->codes), q->scales, q->zeros, q->row_scale};
   };
@@ -383,11 +475,24 @@ cudaError_t launch_w4_stream(int act, const void* a, int64_t a_rows, int K, cons
   // as many warps along K as divide its stages well (idle warps in at most an eighth of the
   // rounds) and have two of them or more a tile, the rest side by side
   const int nst = (K + ST_K - 1) / ST_K;
-  p.WK = ST_WARPS;
+  p.WK = ST_WARPS / 2;                          // RT >= 2: a box of scales is 16 bytes or wider
   while (p.WK > 1 && (2 * p.WK > nst || 8 * nst < 7 * p.WK * ((nst + p.WK - 1) / p.WK)))
     p.WK /= 2;
   p.RT = ST_WARPS / p.WK;
   const int feats = (glu ? 8 : 16) * p.RT;
+  const int gs = ST_K / w->group, groups = (K + w->group - 1) / w->group;
+  p.side_step = (gs * feats + 127) / 128 * 128;
+  if ((int64_t)G * groups > INT32_MAX) return cudaErrorInvalidValue;
+  alignas(64) CUtensorMap c0, c1, s0, s1, z0, z1;
+  auto maps = [&](const moe_w4_t* q, CUtensorMap* c, CUtensorMap* sc, CUtensorMap* z) {
+    if (!make_map_u8(c, q->codes, (uint64_t)G * N, (uint64_t)K / 2, feats, 128, true)) return false;
+    if (!make_map_u8(sc, q->scales, (uint64_t)G * groups, (uint64_t)N, gs, feats, false))
+      return false;
+    return make_map_u8(z, q->zeros ? q->zeros : q->scales, (uint64_t)G * groups, (uint64_t)N, gs,
+                       feats, false);
+  };
+  if (!maps(w, &c0, &s0, &z0) || !maps(glu ? gate : w, &c1, &s1, &z1))
+    return cudaErrorInvalidValue;
   const int64_t tiles = ((a_rows + p.P - 1) / p.P + G) * (int64_t)((N + feats - 1) / feats);
   const int sms = num_sms();
   const int grid = (int)(tiles < sms ? tiles : sms);
@@ -397,7 +502,7 @@ cudaError_t launch_w4_stream(int act, const void* a, int64_t a_rows, int K, cons
     cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(grid), dim3(ST_THREADS), smem, s, c0, c1, p);
+    return launch_pdl(kern, dim3(grid), dim3(ST_THREADS), smem, s, c0, c1, s0, s1, z0, z1, p);
   };
 #define MOE_W4_STREAM(GROUP)                                                               \
   if (w->group == GROUP)                                                                   \
