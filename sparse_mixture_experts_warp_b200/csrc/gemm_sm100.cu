@@ -1473,6 +1473,20 @@ bool make_map_u8(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, 
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_map_u8_3d(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t slices,
+                    uint64_t pitch, uint32_t box_rows, uint32_t box_slices) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  // (a row shorter than a slice: one slice of what there is)
+  const cuuint64_t dims[3] = {pitch < 128 ? pitch : 128, rows, slices};
+  const cuuint64_t strides[2] = {pitch, 128};
+  const cuuint32_t box[3] = {128, box_rows, box_slices};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool gemm_gather_ok() {
   const GemmTile t = gemm_tile();
   return t == TILE_256 || t == TILE_128;

@@ -139,5 +139,10 @@ bool make_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uin
 // x box_rows rows, 128-byte swizzle (box_cols = 128) or none; parts past the end read as zeros.
 bool make_map_u8(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows,
                  uint32_t box_cols, bool swizzle);
+// Host: byte tensor [slices][rows][128] over rows `pitch` bytes apart, slice s at byte 128 s of a
+// row (slices * 128 <= pitch); box = 128 bytes x box_rows rows x box_slices slices, 128-byte
+// swizzle.
+bool make_map_u8_3d(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t slices,
+                    uint64_t pitch, uint32_t box_rows, uint32_t box_slices);
 
 }  // namespace moe

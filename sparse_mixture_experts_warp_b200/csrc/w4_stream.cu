@@ -61,7 +61,6 @@ struct StreamParams {
   int G, N, K, act;
   int P;                                        // tokens per tile
   int RT, WK;
-  int side_step;                                // bytes of a scale box, rounded up to 128
   int fault;                                    // test hook: the first stage of CTA 0 never comes
 };
 
@@ -147,14 +146,17 @@ __device__ __forceinline__ uint32_t to_half2(uint32_t v, float p) {
   return bits(h);
 }
 
+// Per matrix: codes as [whole stages][rows][128 bytes], so that one copy brings what WK warps take
+// (the issue of a copy per warp took longer than the bytes), and as [rows][bytes] for the rounds
+// at K's end; scales and zero points.
+struct StreamMaps {
+  CUtensorMap codes, row_codes, scales, zeros;
+};
+
 template <bool GLU, bool ZEROS, int GROUP>
 __global__ void __launch_bounds__(ST_THREADS, 1)
-w4_stream_kernel(const __grid_constant__ CUtensorMap tmC0,
-                 const __grid_constant__ CUtensorMap tmC1,
-                 const __grid_constant__ CUtensorMap tmS0,
-                 const __grid_constant__ CUtensorMap tmS1,
-                 const __grid_constant__ CUtensorMap tmZ0,
-                 const __grid_constant__ CUtensorMap tmZ1, const StreamParams p) {
+w4_stream_kernel(const __grid_constant__ StreamMaps m0, const __grid_constant__ StreamMaps m1,
+                 const StreamParams p) {
   constexpr int GS = ST_K / GROUP;              // scale groups of a stage
   constexpr int MATS = GLU ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
@@ -241,27 +243,26 @@ w4_stream_kernel(const __grid_constant__ CUtensorMap tmC0,
           break;
         }
         const uint32_t bar = full + 8 * slot;
-        const int n = min(p.WK, nst - s0);      // warps along K that have a stage
         // test hook: armed but never loaded, so the computing warps' wait runs out
         const bool load = !(p.fault == 1 && blockIdx.x == 0 && t == t_lo && s0 == 0);
+        const bool whole = (s0 + p.WK) * ST_K <= p.K;
+        const int n = min(p.WK, nst - s0);      // warps along K that have a stage
         if (leader) {
-          bar_expect(bar, n * MATS * rows * (ST_K / 2 + GS * (ZEROS ? 2 : 1)));
+          bar_expect(bar, MATS * rows * (128 * n + GS * p.WK * (ZEROS ? 2 : 1)));
           if (load) {
-            uint32_t c = smem_u32(smem + slot * ST_STAGE), sc = c + ST_CODES;
-            for (int w = 0; w < n; ++w) {
-              const int x = (s0 + w) * (ST_K / 2), y = tl.g * groups + (s0 + w) * GS;
-              if (GLU) {
-                bar_load(c, &tmC1, bar, x, row);
-                bar_load(sc, &tmS1, bar, tl.n0, y);
-                if (ZEROS) bar_load(sc + ST_SIDE, &tmZ1, bar, tl.n0, y);
-                c += rows * 128;
-                sc += p.side_step;
-              }
-              bar_load(c, &tmC0, bar, x, row);
-              bar_load(sc, &tmS0, bar, tl.n0, y);
-              if (ZEROS) bar_load(sc + ST_SIDE, &tmZ0, bar, tl.n0, y);
-              c += rows * 128;
-              sc += p.side_step;
+            const int y = tl.g * groups + s0 * GS;
+#pragma unroll
+            for (int k = 0; k < MATS; ++k) {    // W_gate, then W_up; or the only matrix
+              const StreamMaps& m = k == MATS - 1 ? m0 : m1;
+              const uint32_t c = smem_u32(smem + slot * ST_STAGE) + k * rows * 128 * p.WK;
+              const uint32_t d = smem_u32(smem + slot * ST_STAGE) + ST_CODES + k * rows * GS * p.WK;
+              if (whole)
+                bar_load_3d(c, &m.codes, bar, 0, row, s0);
+              else
+                for (int w = 0; w < n; ++w)
+                  bar_load(c + w * rows * 128, &m.row_codes, bar, (s0 + w) * (ST_K / 2), row);
+              bar_load(d, &m.scales, bar, tl.n0, y);
+              if (ZEROS) bar_load(d + ST_SIDE, &m.zeros, bar, tl.n0, y);
             }
           }
         }
@@ -289,10 +290,10 @@ w4_stream_kernel(const __grid_constant__ CUtensorMap tmC0,
   const int prow = ((q & 3) << 1) | (q >> 2);   // weight row of fragment row q: reads of the
                                                 // swizzled rows are then free of bank conflicts
   // this lane's bytes of a stage: 16-byte piece 0 of its two rows, and their scales
-  const int code0 = wk * p.RT * 2048 + rt * (GLU ? 1024 : 2048) + prow * 128 + 8 * (c & 1);
-  const int code_up = GLU ? rows * 128 : 1024;
-  const int side0 = ST_CODES + wk * MATS * p.side_step + rt * (GLU ? 8 : 16) + prow;
-  const int side_up = GLU ? p.side_step : 8;
+  const int code0 = wk * rows * 128 + rt * (GLU ? 1024 : 2048) + prow * 128 + 8 * (c & 1);
+  const int code_up = GLU ? rows * 128 * p.WK : 1024;
+  const int side0 = ST_CODES + wk * GS * rows + rt * (GLU ? 8 : 16) + prow;
+  const int side_up = GLU ? rows * GS * p.WK : 8;
   const int lane_at = ((c >> 1) ^ prow) << 4;
   int slot = 0, x_row = -1, xbuf = 0, buf = 0;
   uint32_t phase = 0;
@@ -340,6 +341,13 @@ w4_stream_kernel(const __grid_constant__ CUtensorMap tmC0,
       if (threadIdx.x < ST_TOK) tops[(xbuf ^ 1) * ST_TOK + threadIdx.x] = 0;
       sync_compute();
       x_row = tl.row0;
+    }
+    // the factors of the feature that this thread finishes, under way during the products
+    const int fin = tl.n0 + (threadIdx.x & (feats - 1));
+    float rs_w = 0.f, rs_gate = 0.f;
+    if (fin < p.N) {
+      rs_w = __ldg(p.w.row_scale + (int64_t)tl.g * p.N + fin);
+      if (GLU) rs_gate = __ldg(p.gate.row_scale + (int64_t)tl.g * p.N + fin);
     }
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     // lanes without a token repeat the last one: their columns of the product are not used
@@ -405,33 +413,30 @@ w4_stream_kernel(const __grid_constant__ CUtensorMap tmC0,
     *reinterpret_cast<float2*>(mypart) = make_float2(acc[0], acc[1]);
     *reinterpret_cast<float2*>(mypart + 8 * ST_TOK) = make_float2(acc[2], acc[3]);
     sync_compute();
-    if (rows_ok) {
+    if (rows_ok && fin < p.N) {
       constexpr int per = GLU ? 8 : 16;
-      for (int i = threadIdx.x; i < tl.ntok * feats; i += 32 * ST_WARPS) {
-        const int tok = i >> feats_log, f = i & (feats - 1);
-        const float* src =
-            part + (buf * ST_WARPS + (f / per) * p.WK) * ST_PART + (f % per) * ST_TOK + tok;
-        const int n = tl.n0 + f;
-        if (n >= p.N) continue;
+      const int f = threadIdx.x & (feats - 1);  // (a multiple of feats threads: the same for each
+                                                // of a thread's tokens)
+      const float* src =
+          part + (buf * ST_WARPS + (f / per) * p.WK) * ST_PART + (f % per) * ST_TOK;
+      for (int tok = threadIdx.x >> feats_log; tok < tl.ntok; tok += 32 * ST_WARPS >> feats_log) {
         float v = 0.f, u = 0.f;
+#pragma unroll 4
         for (int w = 0; w < p.WK; ++w) {
-          v += src[w * ST_PART];
-          if (GLU) u += src[w * ST_PART + 8 * ST_TOK];
+          v += src[w * ST_PART + tok];
+          if (GLU) u += src[w * ST_PART + 8 * ST_TOK + tok];
         }
-        const int64_t nr = (int64_t)tl.g * p.N + n;
         const float bk = back[xbuf * ST_TOK + tok];
-        v *= bk;
-        if (GLU) u *= bk;
         if (GLU) {
-          v *= __ldg(p.gate.row_scale + nr);
-          u *= __ldg(p.w.row_scale + nr);
+          v *= bk * rs_gate;
+          u *= bk * rs_w;
           v = __fdividef(v, 1.0f + __expf(-v)) * u;
         } else {
-          v *= __ldg(p.w.row_scale + nr);
+          v *= bk * rs_w;
           if (p.act == MOE_ACT_RELU) v = v < 0.f ? 0.f : v;          // a NaN stays one
           if (p.act == MOE_ACT_GELU) v = 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
         }
-        p.out[((int64_t)tl.row0 + tok) * p.N + n] = __float2bfloat16_rn(v);
+        p.out[((int64_t)tl.row0 + tok) * p.N + fin] = __float2bfloat16_rn(v);
       }
     }
     if (t + 1 < t_hi) tl.next(grp_off, p.N, p.P, feats);
@@ -453,9 +458,12 @@ cudaError_t launch_w4_stream(int act, const void* a, int64_t a_rows, int K, cons
                              cudaStream_t s) {
   if (a_rows <= 0 || G <= 0) return cudaSuccess;
   const bool glu = gate != nullptr;
+  const int gs = ST_K / w->group, groups = (K + w->group - 1) / w->group;
   StreamParams p{};
   p.P = w4_stream_tokens(K, G);
-  if (p.P < 1 || (int64_t)G * N > INT32_MAX) return cudaErrorInvalidValue;
+  // tensor-map coordinates are 32-bit
+  if (p.P < 1 || (int64_t)G * N > INT32_MAX || (int64_t)G * groups > INT32_MAX)
+    return cudaErrorInvalidValue;
   if (a_rows < p.P) p.P = (int)a_rows;
   auto ptrs = [](const moe_w4_t* q) {
     return W4Ptrs{reinterpret_cast<const uint32_t*>(q->codes), q->scales, q->zeros, q->row_scale};
@@ -480,19 +488,16 @@ cudaError_t launch_w4_stream(int act, const void* a, int64_t a_rows, int K, cons
     p.WK /= 2;
   p.RT = ST_WARPS / p.WK;
   const int feats = (glu ? 8 : 16) * p.RT;
-  const int gs = ST_K / w->group, groups = (K + w->group - 1) / w->group;
-  p.side_step = (gs * feats + 127) / 128 * 128;
-  if ((int64_t)G * groups > INT32_MAX) return cudaErrorInvalidValue;
-  alignas(64) CUtensorMap c0, c1, s0, s1, z0, z1;
-  auto maps = [&](const moe_w4_t* q, CUtensorMap* c, CUtensorMap* sc, CUtensorMap* z) {
-    if (!make_map_u8(c, q->codes, (uint64_t)G * N, (uint64_t)K / 2, feats, 128, true)) return false;
-    if (!make_map_u8(sc, q->scales, (uint64_t)G * groups, (uint64_t)N, gs, feats, false))
-      return false;
-    return make_map_u8(z, q->zeros ? q->zeros : q->scales, (uint64_t)G * groups, (uint64_t)N, gs,
+  alignas(64) StreamMaps m0, m1;
+  auto maps = [&](const moe_w4_t* q, StreamMaps* m) {
+    const uint64_t wrows = (uint64_t)G * N, srows = (uint64_t)G * groups, kb = (uint64_t)K / 2;
+    return make_map_u8_3d(&m->codes, q->codes, wrows, K >= ST_K ? K / ST_K : 1, kb, feats, p.WK) &&
+           make_map_u8(&m->row_codes, q->codes, wrows, kb, feats, 128, true) &&
+           make_map_u8(&m->scales, q->scales, srows, (uint64_t)N, gs * p.WK, feats, false) &&
+           make_map_u8(&m->zeros, q->zeros ? q->zeros : q->scales, srows, (uint64_t)N, gs * p.WK,
                        feats, false);
   };
-  if (!maps(w, &c0, &s0, &z0) || !maps(glu ? gate : w, &c1, &s1, &z1))
-    return cudaErrorInvalidValue;
+  if (!maps(w, &m0) || !maps(glu ? gate : w, &m1)) return cudaErrorInvalidValue;
   const int64_t tiles = ((a_rows + p.P - 1) / p.P + G) * (int64_t)((N + feats - 1) / feats);
   const int sms = num_sms();
   const int grid = (int)(tiles < sms ? tiles : sms);
@@ -502,7 +507,7 @@ cudaError_t launch_w4_stream(int act, const void* a, int64_t a_rows, int K, cons
     cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(grid), dim3(ST_THREADS), smem, s, c0, c1, s0, s1, z0, z1, p);
+    return launch_pdl(kern, dim3(grid), dim3(ST_THREADS), smem, s, m0, m1, p);
   };
 #define MOE_W4_STREAM(GROUP)                                                               \
   if (w->group == GROUP)                                                                   \

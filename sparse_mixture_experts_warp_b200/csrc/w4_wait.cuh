@@ -80,4 +80,13 @@ __device__ __forceinline__ void bar_load(uint32_t dst, const CUtensorMap* map, u
   tma_load_2d(dst, map, static_cast<uint64_t*>(__cvta_shared_to_generic(bar)), x, y);
 }
 
+__device__ __forceinline__ void bar_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
 }  // namespace moe
