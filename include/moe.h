@@ -453,7 +453,7 @@ typedef struct moe_w4 {
  *   code = clamp(rint(w * (1 / step)) + zero, 0, 15).
  * A row of zeros (largest t below 2^-100) has row_scale 0; a row that holds a NaN or an infinity
  * stands for NaN.  moe_dequantize_w4 writes the values W stands for, rounded once to dtype.
- * 0 <= n_matrices; n_matrices * N < 2^31. */
+ * 0 <= n_matrices; n_matrices * N < 2^31; K <= 262144. */
 moe_status_t moe_quantize_w4(int32_t n_matrices, int32_t N, int32_t K, int32_t dtype,
                              const void* W, const moe_w4_t* out, moe_stream_t stream);
 moe_status_t moe_dequantize_w4(int32_t n_matrices, int32_t N, int32_t K, const moe_w4_t* w,

@@ -725,7 +725,8 @@ static moe_status_t check_w4_convert(int32_t n, int32_t N, int32_t K, int32_t dt
   if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
   const moe_status_t st = check_w4(w);
   if (st != MOE_OK) return st;
-  if (N % 64 || K % 64 || (int64_t)n * N >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
+  if (N % 64 || K % 64 || K > 262144 || (int64_t)n * N >= ((int64_t)1 << 31))
+    return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

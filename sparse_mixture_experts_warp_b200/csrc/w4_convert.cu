@@ -12,7 +12,13 @@
 // A row that holds a NaN or an infinity gets row_scale NaN or infinity and stands for NaN; a row
 // whose largest t is below 2^-100 counts as zeros (row_scale 0), so 1 / step is always finite.
 //
-// Both directions stream memory: the wide weights once, the 4-bit form once.
+// Both directions stream memory: the wide weights once, the 4-bit form once.  What the instructions
+// may cost beside that (bf16: 4 bytes a clock and SM lane set) shapes both kernels: rounding by
+// adding 1.5 * 2^23 and packing by multiply-add on the sums' bits instead of conversion
+// instructions, a group's three divisions by one lane for the whole group, scales through shared
+// memory (they are stored [group, row]: a row's own are N bytes apart).
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 #include "w4.cuh"
 
@@ -20,6 +26,8 @@ namespace moe {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
+constexpr float kRound = 12582912.f;            // 1.5 * 2^23: x + kRound has rint(x) in its low bits
+constexpr uint32_t kRoundBits = 0x4b400000u;
 
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -35,153 +43,221 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 template <bool BF16> struct Eight;              // eight consecutive weights as stored
 template <> struct Eight<true> {
   uint4 a;
+  __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ void load(const void* base, int64_t i) {
     a = __ldcs(static_cast<const uint4*>(base) + i);
   }
-  __device__ __forceinline__ void widen(float (&w)[8]) const {
+  __device__ __forceinline__ float get(int i) const {
     const uint32_t u[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      w[2 * i] = __uint_as_float(u[i] << 16);
-      w[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
+    return __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
   }
 };
 template <> struct Eight<false> {
   float4 a, b;
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void load(const void* base, int64_t i) {
     a = __ldcs(static_cast<const float4*>(base) + 2 * i);
     b = __ldcs(static_cast<const float4*>(base) + 2 * i + 1);
   }
-  __device__ __forceinline__ void widen(float (&w)[8]) const {
-    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+  __device__ __forceinline__ float get(int i) const {
+    const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    return w[i];
   }
 };
 
-// A block takes one row; a thread eight consecutive k (one word of codes) at a time, so the g / 8
-// threads of a group are neighbouring lanes.  The row is read twice (the second time from
-// cache): once for its largest step, once to quantise.
-constexpr int kQThreads = 128;
+// A block takes `per_block` consecutive rows of a matrix, one after the other, a row with all its
+// warps: a thread holds kWords runs of eight consecutive k (one word of codes each), so the g / 8
+// threads of a group are neighbouring lanes.  Rows longer than the largest block holds are read
+// again for their codes.
+constexpr int kWords = 4;
+constexpr int kMaxWarps = 16;
 
 template <bool BF16, bool ZEROS>
-__global__ void __launch_bounds__(kQThreads)
-quantize_w4_kernel(const void* __restrict__ W, int N, int K, int g, uint32_t* __restrict__ codes,
-                   uint8_t* __restrict__ scales, uint8_t* __restrict__ zeros,
-                   float* __restrict__ row_scale) {
+__global__ void __launch_bounds__(32 * kMaxWarps)
+quantize_w4_kernel(const void* __restrict__ W, int N, int K, int g, int per_block,
+                   uint32_t* __restrict__ codes, uint8_t* __restrict__ scales,
+                   uint8_t* __restrict__ zeros, float* __restrict__ row_scale) {
+  extern __shared__ __align__(16) uint8_t s_side[];             // [groups][per_block] scales, zeros
+  __shared__ float s_max[2][kMaxWarps];
   pdl_trigger();
   pdl_wait();
-  __shared__ float s_max[kQThreads / 32];
-  const int64_t row = blockIdx.x;               // matrix * N + n
-  const int64_t m = row / N;
-  const int n = (int)(row - m * N);
   const int words = K / 8, gw = g / 8, groups = (K + g - 1) / g;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rounds = (words + kQThreads - 1) / kQThreads;
-
-  // the group's raw step t and smallest weight, in every lane of the group
-  auto group_step = [&](const float (&w)[8], float& lo) {
-    float hi = ZEROS ? 0.f : fabsf(w[0]);
-    lo = 0.f;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int64_t row0 = (int64_t)blockIdx.x * per_block;         // matrix * N + n
+  const int64_t m = row0 / N;
+  const int n0 = (int)(row0 - m * N);
+  uint8_t* s_zero = s_side + groups * per_block;
+  const int sub = lane & (gw - 1), pick = sub & (kWords - 1);   // lane of its group, and the word
+                                                                // whose group's divisions it does
+  Eight<BF16> e[kWords];
+  float raw[kWords], lo[kWords];                // a word's group: range, smallest weight (or 0)
+  auto fetch = [&](int64_t row, int base) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      hi = max_nan(hi, ZEROS ? w[i] : fabsf(w[i]));
-      if (ZEROS) lo = min_nan(lo, w[i]);
+    for (int r = 0; r < kWords; ++r) {
+      const int i = base + (r * warps + warp) * 32 + lane;
+      e[r].zero();
+      if (i < words) e[r].load(W, row * words + i);
     }
-    for (int o = 1; o < gw; o <<= 1) {
-      hi = max_nan(hi, __shfl_xor_sync(kFull, hi, o));
-      if (ZEROS) lo = min_nan(lo, __shfl_xor_sync(kFull, lo, o));
-    }
-    return ZEROS ? __fdiv_rn(hi - lo, 15.f) : __fdiv_rn(hi, 7.f);
   };
-
-  float most = 0.f;
-  for (int r = 0; r < rounds; ++r) {
-    const int i = r * kQThreads + threadIdx.x;
-    float w[8] = {}, lo;
-    if (i < words) {
-      Eight<BF16> e;
-      e.load(W, row * words + i);
-      e.widen(w);
+  auto ranges = [&]() {
+#pragma unroll
+    for (int r = 0; r < kWords; ++r) {
+      float hi = ZEROS ? 0.f : fabsf(e[r].get(0));
+      lo[r] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float w = e[r].get(i);
+        hi = max_nan(hi, ZEROS ? w : fabsf(w));
+        if (ZEROS) lo[r] = min_nan(lo[r], w);
+      }
+      for (int o = 1; o < gw; o <<= 1) {
+        hi = max_nan(hi, __shfl_xor_sync(kFull, hi, o));
+        if (ZEROS) lo[r] = min_nan(lo[r], __shfl_xor_sync(kFull, lo[r], o));
+      }
+      raw[r] = ZEROS ? hi - lo[r] : hi;
     }
-    most = max_nan(most, group_step(w, lo));
+  };
+  const int span = kWords * 32 * warps;         // words of a row that the block holds
+  for (int j = 0; j < per_block; ++j) {
+    const int64_t row = row0 + j;
+    float most = 0.f;
+    for (int base = 0; base < words; base += span) {
+      fetch(row, base);
+      ranges();
+#pragma unroll
+      for (int r = 0; r < kWords; ++r) most = max_nan(most, raw[r]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = max_nan(most, __shfl_xor_sync(kFull, most, o));
+    if (warps > 1) {
+      if (lane == 0) s_max[j & 1][warp] = most;
+      __syncthreads();
+      for (int i = 0; i < warps; ++i) most = max_nan(most, s_max[j & 1][i]);
+    }
+    // (division is monotone: the largest range's quotient is the largest quotient)
+    constexpr float kSpread = ZEROS ? 15.f : 7.f;
+    most = __fdiv_rn(most, kSpread);
+    const float rs = most < 0x1p-100f ? 0.f : __fdiv_rn(most, 448.f);
+    if (threadIdx.x == 0) row_scale[row] = rs;
+
+    for (int base = 0; base < words; base += span) {
+      if (words > span) {
+        fetch(row, base);
+        ranges();
+      }
+      // the group of word `pick`, for all of its lanes
+      float my_raw = raw[0], my_lo = lo[0];
+#pragma unroll
+      for (int r = 1; r < kWords; ++r)
+        if (pick == r) {
+          my_raw = raw[r];
+          my_lo = lo[r];
+        }
+      const float t = __fdiv_rn(my_raw, kSpread);
+      const __nv_fp8_e4m3 sc(rs > 0.f ? __fdiv_rn(t, rs) : 0.f);
+      const float step = static_cast<float>(sc) * rs;
+      const float my_inv = step > 0.f ? __fdiv_rn(1.f, step) : 0.f;
+      int my_zero = 8;
+      if (ZEROS) my_zero = (int)fminf(fmaxf(rintf(-my_lo * my_inv), 0.f), 15.f);
+      const int at = base + (pick * warps + warp) * 32 + lane;  // a word of that group
+      if (sub < kWords && at < words) {
+        s_side[at / gw * per_block + j] = sc.__x;
+        if (ZEROS) s_zero[at / gw * per_block + j] = (uint8_t)my_zero;
+      }
+#pragma unroll
+      for (int r = 0; r < kWords; ++r) {
+        const int from = (lane & ~(gw - 1)) + r;
+        const float inv = __shfl_sync(kFull, my_inv, from);
+        const int zero = ZEROS ? __shfl_sync(kFull, my_zero, from) : 8;
+        const int i = base + (r * warps + warp) * 32 + lane;
+        if (i >= words) continue;
+        // clamped, then rounded: the bounds are whole numbers, so the order does not matter; the
+        // sum of the eight rounded ones' bits, 16^p times each, is the word plus a constant
+        const float least = ZEROS ? -(float)zero : -8.f, largest = ZEROS ? 15.f - zero : 7.f;
+        uint32_t word = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float q = fminf(fmaxf(e[r].get(k) * inv, least), largest) + kRound;
+          word += __float_as_uint(q) << (4 * (k / 2 + 4 * (k & 1)));
+        }
+        // sum of kRoundBits 16^p (p = 0..7) is kRoundBits * 0x11111111, and each nibble gets zero
+        word += (uint32_t)zero * 0x11111111u - kRoundBits * 0x11111111u;
+        // words of a block are 8 consecutive k each: k / 8 = 8 b + 4 j + c is word 8 b + 2 c + j
+        const int b = i >> 3, h = (i >> 2) & 1, c = i & 3;
+        codes[row * words + 8 * b + 2 * c + h] = word;
+      }
+    }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) most = max_nan(most, __shfl_xor_sync(kFull, most, o));
-  if (lane == 0) s_max[warp] = most;
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kQThreads / 32; ++i) most = max_nan(most, s_max[i]);
-  const float rs = most < 0x1p-100f ? 0.f : __fdiv_rn(most, 448.f);
-  if (threadIdx.x == 0) row_scale[row] = rs;
-
-  for (int r = 0; r < rounds; ++r) {
-    const int i = r * kQThreads + threadIdx.x;
-    float w[8] = {}, lo;
-    if (i < words) {
-      Eight<BF16> e;
-      e.load(W, row * words + i);
-      e.widen(w);
-    }
-    const float t = group_step(w, lo);
-    if (i >= words) continue;
-    const __nv_fp8_e4m3 sc(rs > 0.f ? __fdiv_rn(t, rs) : 0.f);
-    const float step = static_cast<float>(sc) * rs;
-    const float inv = step > 0.f ? __fdiv_rn(1.f, step) : 0.f;
-    float z = 8.f;
-    if (ZEROS) z = fminf(fmaxf(rintf(-lo * inv), 0.f), 15.f);
-    uint32_t word = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float q = rintf(w[e] * inv);
-      q = ZEROS ? fminf(fmaxf(q + z, 0.f), 15.f) : fminf(fmaxf(q, -8.f), 7.f) + 8.f;
-      word |= (uint32_t)q << (4 * (e / 2 + 4 * (e & 1)));
-    }
-    // words of a block are 8 consecutive k each: k / 8 = 8 b + 4 j + c is word 8 b + 2 c + j
-    const int b = i >> 3, j = (i >> 2) & 1, c = i & 3;
-    codes[row * words + 8 * b + 2 * c + j] = word;
-    if (i % gw == 0) {
-      const int64_t at = (m * groups + i / gw) * N + n;
-      scales[at] = sc.__x;
-      if (ZEROS) zeros[at] = (uint8_t)z;
-    }
+  // the rows' scales (zero points), four rows a word
+  const int quads = per_block / 4;
+  for (int i = threadIdx.x; i < groups * quads; i += blockDim.x) {
+    const int kg = i / quads, n = 4 * (i - kg * quads);
+    const int64_t to = (m * groups + kg) * N + n0 + n;
+    *reinterpret_cast<uint32_t*>(scales + to) =
+        *reinterpret_cast<const uint32_t*>(s_side + kg * per_block + n);
+    if (ZEROS)
+      *reinterpret_cast<uint32_t*>(zeros + to) =
+          *reinterpret_cast<const uint32_t*>(s_zero + kg * per_block + n);
   }
 }
 
-// One word of codes (eight consecutive weights) a thread.
+// A block takes 32 rows by kDqWords words of codes (eight consecutive weights each): their scales
+// through shared memory, then a warp a row at a time.
+constexpr int kDqRows = 32, kDqWords = 64, kDqThreads = 256;
+
 template <bool BF16>
-__global__ void __launch_bounds__(256)
-dequantize_w4_kernel(const W4Ptrs w, int64_t total, int N, int K, int g, void* __restrict__ out) {
+__global__ void __launch_bounds__(kDqThreads)
+dequantize_w4_kernel(const W4Ptrs w, int N, int K, int g, void* __restrict__ out) {
   pdl_trigger();
   pdl_wait();
+  __shared__ uint32_t s_scale[16][kDqRows / 4], s_zero[16][kDqRows / 4];
   const int words = K / 8, groups = (K + g - 1) / g;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t row = i / words;              // i: 8 weights from k = 8 kw on
-    const int kw = (int)(i - row * words);
-    const int64_t m = row / N;
-    const int n = (int)(row - m * N);
-    const int b = kw >> 3, j = (kw >> 2) & 1, c = kw & 3;
-    const uint32_t word = w.codes[row * words + 8 * b + 2 * c + j];
-    const int64_t at = (m * groups + 8 * kw / g) * N + n;
-    const float sc = w4_scale(w.scales[at]), rs = w.row_scale[row];
-    const float z = w.zeros ? (float)w.zeros[at] : 8.f;
-    float v[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row0 = (int64_t)blockIdx.x * kDqRows;           // matrix * N + n
+  const int64_t m = row0 / N;
+  const int n0 = (int)(row0 - m * N), w0 = blockIdx.y * kDqWords;
+  const int kg0 = 8 * w0 / g, here = min(kDqWords * 8 / g, groups - kg0);
+  if (threadIdx.x < here * (kDqRows / 4)) {
+    const int kg = threadIdx.x / (kDqRows / 4), i = threadIdx.x % (kDqRows / 4);
+    const int64_t at = (m * groups + kg0 + kg) * N + n0 + 4 * i;
+    s_scale[kg][i] = *reinterpret_cast<const uint32_t*>(w.scales + at);
+    s_zero[kg][i] = w.zeros ? *reinterpret_cast<const uint32_t*>(w.zeros + at) : 0x08080808u;
+  }
+  __syncthreads();
+#pragma unroll 4
+  for (int r = warp; r < kDqRows; r += kDqThreads / 32) {
+    const int64_t row = row0 + r;
+    const float rs = __ldg(w.row_scale + row);
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      v[e] = rs * (sc * ((float)((word >> (4 * (e / 2 + 4 * (e & 1)))) & 15u) - z));
-    if (BF16) {
-      uint32_t p[4];
+    for (int half = 0; half < kDqWords / 32; ++half) {
+      const int i = w0 + 32 * half + lane;      // word 2 c + j of block b holds k = 32 j + 8 c
+      if (i >= words) continue;
+      const uint32_t word = __ldcs(w.codes + row * words + i);
+      const int k = (i >> 3) * W4_BLOCK + w4_word_k(i & 7);
+      const int kg = k / g - kg0;
+      const float sc = w4_scale((s_scale[kg][r / 4] >> (8 * (r & 3))) & 0xffu);
+      const uint32_t z = (s_zero[kg][r / 4] >> (8 * (r & 3))) & 0xffu;
+      // 2^23 + code as a float's bits, minus 2^23 + zero: exact, as is the product with sc
+      const float zf = __uint_as_float(0x4b000000u + z);
+      float v[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-        p[e] = *reinterpret_cast<const uint32_t*>(&h);
+      for (int e = 0; e < 8; ++e)
+        v[e] = rs * (sc * (__uint_as_float(
+                               ((word >> (4 * (e / 2 + 4 * (e & 1)))) & 15u) | 0x4b000000u) - zf));
+      if (BF16) {
+        uint32_t p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+          p[e] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        __stcs(static_cast<uint4*>(out) + (row * K + k) / 8, make_uint4(p[0], p[1], p[2], p[3]));
+      } else {
+        float4* o = static_cast<float4*>(out) + (row * K + k) / 4;
+        __stcs(o, make_float4(v[0], v[1], v[2], v[3]));
+        __stcs(o + 1, make_float4(v[4], v[5], v[6], v[7]));
       }
-      __stcs(static_cast<uint4*>(out) + i, make_uint4(p[0], p[1], p[2], p[3]));
-    } else {
-      float4* o = static_cast<float4*>(out) + 2 * i;
-      __stcs(o, make_float4(v[0], v[1], v[2], v[3]));
-      __stcs(o + 1, make_float4(v[4], v[5], v[6], v[7]));
     }
   }
 }
@@ -190,21 +266,34 @@ dequantize_w4_kernel(const W4Ptrs w, int64_t total, int N, int K, int g, void* _
 
 cudaError_t launch_quantize_w4(int n_matrices, int N, int K, bool bf16, const void* W,
                                const moe_w4_t& o, cudaStream_t s) {
-  const dim3 grid((unsigned)((int64_t)n_matrices * N)), block(kQThreads);
+  const int64_t rows = (int64_t)n_matrices * N;
+  const int words = K / 8, groups = (K + o.group - 1) / o.group;
+  int warps = (words + 32 * kWords - 1) / (32 * kWords);
+  if (warps > kMaxWarps) warps = kMaxWarps;
+  // rows per block: 32 fill a sector of scales; fewer when the blocks would not fill the SMs a
+  // few times over, or their scales 48 KB of shared memory (N is a multiple of 64)
+  int per = 32;
+  const size_t side = (size_t)groups * (o.zeros ? 2 : 1);
+  while (per > 4 && (rows / per < (int64_t)num_sms() * 16 || side * per > 40960)) per /= 2;
+  const size_t smem = side * per;
   auto k = bf16 ? (o.zeros ? quantize_w4_kernel<true, true> : quantize_w4_kernel<true, false>)
                 : (o.zeros ? quantize_w4_kernel<false, true> : quantize_w4_kernel<false, false>);
-  return launch_pdl(k, grid, block, 0, s, W, N, K, o.group, reinterpret_cast<uint32_t*>(o.codes),
-                    o.scales, o.zeros, o.row_scale);
+  if (smem > 40960) {
+    cudaError_t e =
+        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(k, dim3((unsigned)(rows / per)), dim3(32 * warps), smem, s, W, N, K, o.group,
+                    per, reinterpret_cast<uint32_t*>(o.codes), o.scales, o.zeros, o.row_scale);
 }
 
 cudaError_t launch_dequantize_w4(int n_matrices, int N, int K, const moe_w4_t& w, bool bf16,
                                  void* out, cudaStream_t s) {
-  const int64_t total = (int64_t)n_matrices * N * (K / 8);
-  const int64_t blocks = (total + 255) / 256, most = (int64_t)num_sms() * 16;
-  const dim3 grid((unsigned)(blocks < most ? blocks : most)), block(256);
+  const int64_t rows = (int64_t)n_matrices * N;
+  const dim3 grid((unsigned)(rows / kDqRows), (unsigned)((K / 8 + kDqWords - 1) / kDqWords));
   const W4Ptrs p{reinterpret_cast<const uint32_t*>(w.codes), w.scales, w.zeros, w.row_scale};
   auto k = bf16 ? dequantize_w4_kernel<true> : dequantize_w4_kernel<false>;
-  return launch_pdl(k, grid, block, 0, s, p, total, N, K, w.group, out);
+  return launch_pdl(k, grid, dim3(kDqThreads), 0, s, p, N, K, w.group, out);
 }
 
 }  // namespace moe
