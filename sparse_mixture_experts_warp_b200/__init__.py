@@ -211,7 +211,8 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # torch.cuda.current_stream().cuda_stream without the Stream object (3 us a call)
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -438,11 +439,14 @@ def moe_layer_forward_train(d, x, Wg, sel_bias, W_gate, W_up, W_down, out, ws, b
 
 def _here(*tensors):
     """Refuses tensors that are not on the current CUDA device (None and addresses pass)."""
+    now = None
     for t in tensors:
-        if isinstance(t, torch.Tensor) and not (
-                t.is_cuda and t.get_device() == torch.cuda.current_device()):
-            raise ValueError(f"a tensor on {t.device} was handed to the MoE library, which runs "
-                             "on the current CUDA device")
+        if isinstance(t, torch.Tensor):
+            if now is None and t.is_cuda:
+                now = torch.cuda.current_device()
+            if not t.is_cuda or t.get_device() != now:
+                raise ValueError(f"a tensor on {t.device} was handed to the MoE library, which "
+                                 "runs on the current CUDA device")
 
 
 # ------------------------------------ gradients of the dispatch and merge ----

@@ -17,7 +17,7 @@
 // adding 1.5 * 2^23 and packing by multiply-add on the sums' bits instead of conversion
 // instructions, a group's three divisions by one lane for the whole group, scales through shared
 // memory (they are stored [group, row]: a row's own are N bytes apart).
-#include <cuda_fp16.h>
+#include <float.h>
 
 #include "common.cuh"
 #include "w4.cuh"
@@ -51,6 +51,21 @@ template <> struct Eight<true> {
     const uint32_t u[4] = {a.x, a.y, a.z, a.w};
     return __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
   }
+  // largest (magnitude, or weight and 0) and smallest (weight and 0), two at a time; NaN stay
+  template <bool ZEROS>
+  __device__ __forceinline__ void range(float& hi, float& lo) const {
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+    const __nv_bfloat162 none = __floats2bfloat162_rn(0.f, 0.f);
+    __nv_bfloat162 most = none, least = none;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&u[i]);
+      most = __hmax2_nan(most, ZEROS ? v : __habs2(v));
+      if (ZEROS) least = __hmin2_nan(least, v);
+    }
+    hi = max_nan(__low2float(most), __high2float(most));
+    lo = ZEROS ? min_nan(__low2float(least), __high2float(least)) : 0.f;
+  }
 };
 template <> struct Eight<false> {
   float4 a, b;
@@ -62,6 +77,15 @@ template <> struct Eight<false> {
   __device__ __forceinline__ float get(int i) const {
     const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     return w[i];
+  }
+  template <bool ZEROS>
+  __device__ __forceinline__ void range(float& hi, float& lo) const {
+    hi = lo = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      hi = max_nan(hi, ZEROS ? get(i) : fabsf(get(i)));
+      if (ZEROS) lo = min_nan(lo, get(i));
+    }
   }
 };
 
@@ -102,14 +126,8 @@ quantize_w4_kernel(const void* __restrict__ W, int N, int K, int g, int per_bloc
   auto ranges = [&]() {
 #pragma unroll
     for (int r = 0; r < kWords; ++r) {
-      float hi = ZEROS ? 0.f : fabsf(e[r].get(0));
-      lo[r] = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float w = e[r].get(i);
-        hi = max_nan(hi, ZEROS ? w : fabsf(w));
-        if (ZEROS) lo[r] = min_nan(lo[r], w);
-      }
+      float hi;
+      e[r].template range<ZEROS>(hi, lo[r]);
       for (int o = 1; o < gw; o <<= 1) {
         hi = max_nan(hi, __shfl_xor_sync(kFull, hi, o));
         if (ZEROS) lo[r] = min_nan(lo[r], __shfl_xor_sync(kFull, lo[r], o));
@@ -159,6 +177,11 @@ quantize_w4_kernel(const void* __restrict__ W, int N, int K, int g, int per_bloc
       const float my_inv = step > 0.f ? __fdiv_rn(1.f, step) : 0.f;
       int my_zero = 8;
       if (ZEROS) my_zero = (int)fminf(fmaxf(rintf(-my_lo * my_inv), 0.f), 15.f);
+      // a scale that is a normal e4m3 (from 2^-6 on, byte 8) is off by at most a 16th, so |w r| is
+      // below 7.5 and its rounding needs no clamp; nor where the codes do not matter (r = 0), but
+      // an infinity or a NaN has to stay in its nibble
+      const bool clamp =
+          __any_sync(kFull, !(my_raw <= FLT_MAX) || (sc.__x < 8 && my_inv > 0.f));
       const int at = base + (pick * warps + warp) * 32 + lane;  // a word of that group
       if (sub < kWords && at < words) {
         s_side[at / gw * per_block + j] = sc.__x;
@@ -175,10 +198,17 @@ quantize_w4_kernel(const void* __restrict__ W, int N, int K, int g, int per_bloc
         // sum of the eight rounded ones' bits, 16^p times each, is the word plus a constant
         const float least = ZEROS ? -(float)zero : -8.f, largest = ZEROS ? 15.f - zero : 7.f;
         uint32_t word = 0;
+        if (ZEROS || clamp) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float q = fminf(fmaxf(e[r].get(k) * inv, least), largest) + kRound;
-          word += __float_as_uint(q) << (4 * (k / 2 + 4 * (k & 1)));
+          for (int k = 0; k < 8; ++k) {
+            const float q = fminf(fmaxf(e[r].get(k) * inv, least), largest) + kRound;
+            word += __float_as_uint(q) << (4 * (k / 2 + 4 * (k & 1)));
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            word += __float_as_uint(__fadd_rn(__fmul_rn(e[r].get(k), inv), kRound))   // (not fused)
+                    << (4 * (k / 2 + 4 * (k & 1)));
         }
         // sum of kRoundBits 16^p (p = 0..7) is kRoundBits * 0x11111111, and each nibble gets zero
         word += (uint32_t)zero * 0x11111111u - kRoundBits * 0x11111111u;
@@ -225,36 +255,40 @@ dequantize_w4_kernel(const W4Ptrs w, int N, int K, int g, void* __restrict__ out
     s_zero[kg][i] = w.zeros ? *reinterpret_cast<const uint32_t*>(w.zeros + at) : 0x08080808u;
   }
   __syncthreads();
-#pragma unroll 4
-  for (int r = warp; r < kDqRows; r += kDqThreads / 32) {
+  const int b = w0 / 8 + lane / 4, c = lane & 3;  // block, and the words 2 c, 2 c + 1 in it: k from
+  const bool live = 8 * b < words;              // 8 c and from 32 + 8 c on
+  const int k0 = 64 * b + 8 * c, kg = live ? k0 / g - kg0 : 0, kg1 = live ? (k0 + 32) / g - kg0 : 0;
+#pragma unroll
+  for (int i = 0; i < kDqRows / (kDqThreads / 32); ++i) {
+    const int r = warp + i * (kDqThreads / 32);
     const int64_t row = row0 + r;
+    if (!live) continue;
+    const uint2 word = __ldcs(reinterpret_cast<const uint2*>(w.codes + row * words + 8 * b) + c);
     const float rs = __ldg(w.row_scale + row);
 #pragma unroll
-    for (int half = 0; half < kDqWords / 32; ++half) {
-      const int i = w0 + 32 * half + lane;      // word 2 c + j of block b holds k = 32 j + 8 c
-      if (i >= words) continue;
-      const uint32_t word = __ldcs(w.codes + row * words + i);
-      const int k = (i >> 3) * W4_BLOCK + w4_word_k(i & 7);
-      const int kg = k / g - kg0;
-      const float sc = w4_scale((s_scale[kg][r / 4] >> (8 * (r & 3))) & 0xffu);
-      const uint32_t z = (s_zero[kg][r / 4] >> (8 * (r & 3))) & 0xffu;
+    for (int h = 0; h < 2; ++h) {
+      const int shift = 8 * (r & 3);
+      const float sc = w4_scale((s_scale[h ? kg1 : kg][r / 4] >> shift) & 0xffu);
       // 2^23 + code as a float's bits, minus 2^23 + zero: exact, as is the product with sc
-      const float zf = __uint_as_float(0x4b000000u + z);
+      const float zf =
+          __uint_as_float(0x4b000000u + ((s_zero[h ? kg1 : kg][r / 4] >> shift) & 0xffu));
+      const uint32_t u = h ? word.y : word.x;
       float v[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        v[e] = rs * (sc * (__uint_as_float(
-                               ((word >> (4 * (e / 2 + 4 * (e & 1)))) & 15u) | 0x4b000000u) - zf));
+        v[e] = rs * (sc * (__uint_as_float(((u >> (4 * (e / 2 + 4 * (e & 1)))) & 15u) |
+                                           0x4b000000u) - zf));
+      const int64_t at = row * K + k0 + 32 * h;
       if (BF16) {
         uint32_t p[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-          p[e] = *reinterpret_cast<const uint32_t*>(&h);
+          const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+          p[e] = *reinterpret_cast<const uint32_t*>(&x);
         }
-        __stcs(static_cast<uint4*>(out) + (row * K + k) / 8, make_uint4(p[0], p[1], p[2], p[3]));
+        __stcs(static_cast<uint4*>(out) + at / 8, make_uint4(p[0], p[1], p[2], p[3]));
       } else {
-        float4* o = static_cast<float4*>(out) + (row * K + k) / 4;
+        float4* o = static_cast<float4*>(out) + at / 4;
         __stcs(o, make_float4(v[0], v[1], v[2], v[3]));
         __stcs(o + 1, make_float4(v[4], v[5], v[6], v[7]));
       }
