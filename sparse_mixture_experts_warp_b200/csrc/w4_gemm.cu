@@ -23,7 +23,7 @@
 //                boxes of 64 k (128-byte swizzle);
 //   warp 2       MMA issuer (tcgen05.mma kind::f16, A from tensor memory) and TMEM owner;
 //   warp 3       group table;
-//   warps 4..    dequantisers: 4 * W4_DQ_SETS warps, each set of four takes every W4_DQ_SETS-th
+//   warps 4..    dequantisers: 4 * DQ warps, each set of four takes every DQ-th
 //                128-element k-block, thread by thread 16 words -> 64 columns of packed bf16
 //                pairs (tcgen05.st), into a ring of 4 A stages of 64 columns;
 //   then         epilogue: tcgen05.ld, row factor, activation, bf16 stores.
@@ -52,26 +52,30 @@ constexpr int W4_KA = 128;                      // k of an A stage
 constexpr int W4_CODE_BYTES = W4_ROWS * W4_KS / 2;
 constexpr int W4_SIDE_BYTES = 1024;             // scales (or zero points) of a stage: 8 x 128
 constexpr int W4_W_STAGE = W4_CODE_BYTES + 2 * W4_SIDE_BYTES;
-constexpr int W4_XBOX = 32;                     // token rows per box
-constexpr int W4_XBOX_BYTES = W4_XBOX * W4_KB * 2;
-constexpr int W4_A_STAGES = 4;
 constexpr int W4_A_COLS = W4_KA / 2;
-constexpr int W4_ACC_COLS = 256;
 constexpr int W4_TMEM_COLS = 512;
-// A stage of the A ring belongs to one set of dequantisers: another set could be two rounds ahead of
-// it and take the wait's parity for its own.
-constexpr int W4_DQ_SETS = 4;
-static_assert(W4_A_STAGES % W4_DQ_SETS == 0, "a stage has one set of dequantisers");
-constexpr int W4_EPI_SETS = 1;
 constexpr int W4_FIRST_DQ = 4;
-constexpr int W4_FIRST_EPI = W4_FIRST_DQ + 4 * W4_DQ_SETS;
-constexpr int W4_THREADS = 32 * (W4_FIRST_EPI + 4 * W4_EPI_SETS);
 
-// Tokens of a tile, weight stages, token stages and their k, accumulators.
+// Tokens of a tile; weight stages; token stages, their k and the rows of their boxes; accumulators;
+// A stages; sets of four dequantisers and of four epilogue warps.  A stage of the A ring belongs
+// to one set of dequantisers: another set could be two rounds ahead of it and take the wait's
+// parity for its own.
 template <int NT> struct W4Shape;
-template <> struct W4Shape<256> { static constexpr int WS = 3, XS = 5, XK = 64, ACCS = 1; };
-template <> struct W4Shape<128> { static constexpr int WS = 5, XS = 3, XK = 128, ACCS = 2; };
-template <> struct W4Shape<32> { static constexpr int WS = 8, XS = 4, XK = 256, ACCS = 2; };
+template <> struct W4Shape<192> {
+  static constexpr int WS = 3, XS = 6, XK = 64, XBOX = 64, ACCS = 2, AS = 2, DQ = 2, EPI = 2;
+};
+template <> struct W4Shape<128> {
+  static constexpr int WS = 5, XS = 3, XK = 128, XBOX = 64, ACCS = 2, AS = 4, DQ = 4, EPI = 1;
+};
+template <> struct W4Shape<32> {
+  static constexpr int WS = 8, XS = 4, XK = 256, XBOX = 32, ACCS = 2, AS = 4, DQ = 4, EPI = 1;
+};
+template <int NT> constexpr int w4_threads() {
+  using S = W4Shape<NT>;
+  static_assert(S::AS % S::DQ == 0, "an A stage has one set of dequantisers");
+  static_assert(S::ACCS * (NT < 128 ? 128 : NT) + S::AS * W4_A_COLS <= W4_TMEM_COLS, "TMEM columns");
+  return 32 * (W4_FIRST_DQ + 4 * S::DQ + 4 * S::EPI);
+}
 
 struct W4Params {
   const int32_t* offsets;                       // [G + 1] device
@@ -97,13 +101,14 @@ __device__ __forceinline__ W4Tile w4_locate(int t, const int* grp_off, const int
   while (t >= tile_pre[g + 1]) ++g;
   const int m = grp_off[g + 1] - grp_off[g];
   const int mt = (m + NT - 1) / NT;
+  const int per = ((m + mt - 1) / mt + 15) & ~15;     // rows of a token tile, alike for all
   const int local = t - tile_pre[g];
   W4Tile r;
   r.g = g;
   r.n_idx = local / mt;
   const int j = local - r.n_idx * mt;
-  r.ntok = min(NT, m - j * NT);
-  r.row0 = grp_off[g] + j * NT;
+  r.ntok = min(per, m - j * per);
+  r.row0 = grp_off[g] + j * per;
   return r;
 }
 
@@ -164,13 +169,18 @@ __device__ __forceinline__ void dequant_word(uint32_t w, __nv_bfloat162 z, __nv_
 }
 
 template <int NT, bool GLU>
-__global__ void __launch_bounds__(W4_THREADS, 1)
+__global__ void __launch_bounds__(w4_threads<NT>(), 1)
 w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmC0,
                const __grid_constant__ CUtensorMap tmC1, const __grid_constant__ CUtensorMap tmS0,
                const __grid_constant__ CUtensorMap tmS1, const __grid_constant__ CUtensorMap tmZ0,
                const __grid_constant__ CUtensorMap tmZ1, const W4Params p) {
   constexpr int WS = W4Shape<NT>::WS, XS = W4Shape<NT>::XS, XK = W4Shape<NT>::XK,
-                ACCS = W4Shape<NT>::ACCS;
+                ACCS = W4Shape<NT>::ACCS, AS = W4Shape<NT>::AS, DQ = W4Shape<NT>::DQ,
+                EPI = W4Shape<NT>::EPI, XBOX = W4Shape<NT>::XBOX;
+  constexpr int ACC_PITCH = NT < 128 ? 128 : NT;      // columns between accumulators
+  constexpr int A_COL = ACCS * ACC_PITCH;             // first column of the A ring
+  constexpr int FIRST_EPI = W4_FIRST_DQ + 4 * DQ;
+  constexpr int XBOX_BYTES = XBOX * W4_KB * 2;
   constexpr int XB = XK / W4_KB;                // 64-element boxes of a token stage
   constexpr int X_BOX = NT * W4_KB * 2;
   constexpr int X_STAGE = XB * X_BOX;
@@ -180,7 +190,7 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* ws = smem + XS * X_STAGE;            // token stages, then weight stages
   uint64_t* bars = reinterpret_cast<uint64_t*>(ws + WS * W4_W_STAGE);
-  constexpr int BARS = 2 * (WS + XS + W4_A_STAGES + ACCS) + 1;
+  constexpr int BARS = 2 * (WS + XS + AS + ACCS) + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* grp_off = reinterpret_cast<int*>(tmem_holder + 2);       // [G + 1]
@@ -188,8 +198,8 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
   const uint32_t xs = smem_u32(smem);
   const uint32_t w_full = smem_u32(bars), w_empty = w_full + 8 * WS;
   const uint32_t x_full = w_empty + 8 * WS, x_empty = x_full + 8 * XS;
-  const uint32_t a_full = x_empty + 8 * XS, a_empty = a_full + 8 * W4_A_STAGES;
-  const uint32_t t_full = a_empty + 8 * W4_A_STAGES, t_empty = t_full + 8 * ACCS;
+  const uint32_t a_full = x_empty + 8 * XS, a_empty = a_full + 8 * AS;
+  const uint32_t t_full = a_empty + 8 * AS, t_empty = t_full + 8 * ACCS;
   const uint32_t drain = t_empty + 8 * ACCS;
   const BarWait wait{abort_flag, p.err};
 
@@ -200,12 +210,12 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
       for (int i = 0; i < n; ++i) mbar_init(b++, count);
     };
     init(WS, 1);
-    init(WS, 4 * W4_DQ_SETS);
+    init(WS, 4 * DQ);
     init(2 * XS, 1);
-    init(W4_A_STAGES, 4);
-    init(W4_A_STAGES, 1);
+    init(AS, 4);
+    init(AS, 1);
     init(ACCS, 1);
-    init(ACCS, 4 * W4_EPI_SETS);
+    init(ACCS, 4 * EPI);
     init(1, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -319,7 +329,7 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     bool ok = true;
     for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
       const W4Tile tl = w4_locate<NT>(t, grp_off, tile_pre, g);
-      const int nbox = (tl.ntok + W4_XBOX - 1) / W4_XBOX;
+      const int nbox = (tl.ntok + XBOX - 1) / XBOX;
       for (int kb = 0; kb < nkb; kb += XB) {
         if (!wait(x_empty + 8 * stage, phase ^ 1u, DEVERR_TIMEOUT_TMA)) {
           ok = false;
@@ -328,11 +338,11 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         const uint32_t bar = x_full + 8 * stage;
         const int here = min(XB, nkb - kb);
         if (leader) {
-          bar_expect(bar, here * nbox * W4_XBOX_BYTES);
+          bar_expect(bar, here * nbox * XBOX_BYTES);
           for (int h = 0; h < here; ++h)
             for (int b = 0; b < nbox; ++b)
-              bar_load(xs + stage * X_STAGE + h * X_BOX + b * W4_XBOX_BYTES, &tmX, bar,
-                       (kb + h) * W4_KB, tl.row0 + b * W4_XBOX);
+              bar_load(xs + stage * X_STAGE + h * X_BOX + b * XBOX_BYTES, &tmX, bar,
+                       (kb + h) * W4_KB, tl.row0 + b * XBOX);
         }
         issued |= 1u << stage;
         issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
@@ -356,7 +366,7 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
       const uint32_t idesc =
           idesc_bf16(W4_ROWS, __shfl_sync(kFullWarp, (tl.ntok + 15) & ~15, 0));
       const int acc = it % ACCS;
-      const uint32_t d = tmem_base + acc * (W4_ACC_COLS / ACCS);
+      const uint32_t d = tmem_base + acc * ACC_PITCH;
       if (!wait(t_empty + 8 * acc, (uint32_t)((it / ACCS) & 1) ^ 1u, DEVERR_TIMEOUT_MMA)) {
         ok = false;
         break;
@@ -367,7 +377,7 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
           ok = false;
           break;
         }
-        const uint32_t a0 = tmem_base + W4_ACC_COLS + ast * W4_A_COLS;
+        const uint32_t a0 = tmem_base + A_COL + ast * W4_A_COLS;
 #pragma unroll
         for (int h = 0; h < W4_KA / W4_KB; ++h) {
           if (kb + h >= nkb) break;
@@ -392,7 +402,7 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
           }
         }
         if (leader) bar_commit(a_empty + 8 * ast);
-        if (++ast == W4_A_STAGES) {
+        if (++ast == AS) {
           ast = 0;
           aph ^= 1u;
         }
@@ -402,7 +412,7 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     // all MMAs issued by this thread complete before the CTA releases TMEM
     if (leader) bar_commit(drain);
     wait.drain(drain, 0u, DEVERR_TIMEOUT_MMA, ok ? kWaitNs : kDrainNs);
-  } else if (warp >= W4_FIRST_DQ && warp < W4_FIRST_EPI) {
+  } else if (warp >= W4_FIRST_DQ && warp < FIRST_EPI) {
     // ---------------- dequantisers ----------------
     const int q = warp & 3, set = (warp - W4_FIRST_DQ) >> 2;
     // row of the stage's codes, and where its scales start and step
@@ -410,7 +420,7 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     const int side = GLU ? (lane & 16) * (W4_SIDE_BYTES / 32) + 16 * q + (lane & 15) : row;
     const int pitch = GLU ? 64 : 128;
     const int shift = p.group == 32 ? 5 : p.group == 64 ? 6 : 7;
-    const uint32_t trow = tmem_base + W4_ACC_COLS + ((uint32_t)(32 * q) << 16);
+    const uint32_t trow = tmem_base + A_COL + ((uint32_t)(32 * q) << 16);
     int wst = 0, ast = 0;
     uint32_t wph = 0, aph = 1, turn = 0;        // turn: A stages before this one, over all tiles
     bool ok = true;
@@ -425,7 +435,7 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         const uint8_t* zp = sc + W4_SIDE_BYTES;
         const int here = min(4, nkb - 4 * s);
         for (int b0 = 0; b0 < here; b0 += W4_KA / W4_KB, ++turn) {
-          if (turn % W4_DQ_SETS == set) {
+          if (turn % DQ == set) {
             // everything of the A stage's 128 k first: codes, scales, zero points (a block past K
             // is read as zeros or the next matrix's scales, and no MMA takes it)
             const uint8_t* src = st + row * 128;
@@ -477,7 +487,7 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
             __syncwarp();
             if (lane == 0) bar_arrive(a_full + 8 * ast);
           }
-          if (++ast == W4_A_STAGES) {
+          if (++ast == AS) {
             ast = 0;
             aph ^= 1u;
           }
@@ -490,9 +500,9 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         }
       }
     }
-  } else if (warp >= W4_FIRST_EPI) {
+  } else if (warp >= FIRST_EPI) {
     // ---------------- epilogue ----------------
-    const int q = warp & 3, set = (warp - W4_FIRST_EPI) >> 2;
+    const int q = warp & 3, set = (warp - FIRST_EPI) >> 2;
     int g = 0, it = 0;
     for (int t = blockIdx.x; t < total; t += gridDim.x, ++it) {
       const W4Tile tl = w4_locate<NT>(t, grp_off, tile_pre, g);
@@ -506,10 +516,10 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
       const bool rows_ok = tl.row0 >= 0 && (int64_t)tl.row0 + tl.ntok <= p.rows;
       if (!rows_ok && lane == 0) atomicCAS(p.err, 0, DEVERR_BOUNDS);
       const bool st = rows_ok && feat < p.N;
-      const uint32_t d = tmem_base + acc * (W4_ACC_COLS / ACCS) + ((uint32_t)(32 * q) << 16);
+      const uint32_t d = tmem_base + acc * ACC_PITCH + ((uint32_t)(32 * q) << 16);
       __nv_bfloat16* o = p.out + (int64_t)tl.row0 * p.N + feat;
 #pragma unroll 1
-      for (int c = 16 * set; c < tl.ntok; c += 16 * W4_EPI_SETS) {
+      for (int c = 16 * set; c < tl.ntok; c += 16 * EPI) {
         uint32_t v[16];
         tmem_ld16(d + c, v);
         tmem_wait_ld();
@@ -557,7 +567,7 @@ template <int NT>
 size_t w4_smem(int G) {
   using S = W4Shape<NT>;
   return 1024 + (size_t)S::XS * NT * S::XK * 2 + (size_t)S::WS * W4_W_STAGE +
-         (2 * S::WS + 2 * S::XS + 2 * W4_A_STAGES + 2 * S::ACCS + 1) * 8 + 8 +
+         (2 * S::WS + 2 * S::XS + 2 * S::AS + 2 * S::ACCS + 1) * 8 + 8 +
          (size_t)2 * (G + 1) * sizeof(int);
 }
 
@@ -575,7 +585,7 @@ cudaError_t launch(const W4Maps& m, const W4Params& p, int64_t a_rows, cudaStrea
   const int64_t most = ((a_rows + NT - 1) / NT + p.G) * (int64_t)p.nt;
   const int sms = gemm_sm_count();
   const int grid = (int)(most < sms ? most : sms);
-  return launch_pdl(kern, dim3(grid), dim3(W4_THREADS), smem, s, m.x, m.c0, m.c1, m.s0, m.s1, m.z0,
+  return launch_pdl(kern, dim3(grid), dim3(w4_threads<NT>()), smem, s, m.x, m.c0, m.c1, m.s0, m.s1, m.z0,
                     m.z1, p);
 }
 
@@ -591,6 +601,9 @@ cudaError_t launch_w4_gemm(int act, const void* a, int64_t a_rows, int K, const 
     return cudaErrorInvalidValue;
   const bool glu = gate != nullptr;
   const int feats = glu ? 64 : 128;
+  const int64_t mean = (a_rows + G - 1) / G;
+  const int nt_tok = mean > 128 ? 192 : mean > 24 ? 128 : 32;
+  const int xbox = nt_tok == 32 ? W4Shape<32>::XBOX : W4Shape<128>::XBOX;
   alignas(64) W4Maps m;
   auto maps = [&](const moe_w4_t* q, CUtensorMap* c, CUtensorMap* sc, CUtensorMap* z) {
     const int gs = W4_KS / q->group;
@@ -600,7 +613,7 @@ cudaError_t launch_w4_gemm(int act, const void* a, int64_t a_rows, int K, const 
     return make_map_u8(z, q->zeros ? q->zeros : q->scales, (uint64_t)G * groups, (uint64_t)N, gs,
                        feats, false);
   };
-  if (!make_map(&m.x, a, (uint64_t)a_rows, (uint64_t)K, W4_XBOX, W4_KB) ||
+  if (!make_map(&m.x, a, (uint64_t)a_rows, (uint64_t)K, xbox, W4_KB) ||
       !maps(w, &m.c0, &m.s0, &m.z0) || !maps(glu ? gate : w, &m.c1, &m.s1, &m.z1))
     return cudaErrorInvalidValue;
   W4Params p{};
@@ -618,10 +631,9 @@ cudaError_t launch_w4_gemm(int act, const void* a, int64_t a_rows, int K, const 
   p.zeros = w->zeros ? 1 : 0;
   p.nt = (N + feats - 1) / feats;
   p.fault = gemm_fault();
-  const int64_t mean = (a_rows + G - 1) / G;
-  if (mean > 128)
-    return glu ? launch<256, true>(m, p, a_rows, s) : launch<256, false>(m, p, a_rows, s);
-  if (mean > 24)
+  if (nt_tok == 192)
+    return glu ? launch<192, true>(m, p, a_rows, s) : launch<192, false>(m, p, a_rows, s);
+  if (nt_tok == 128)
     return glu ? launch<128, true>(m, p, a_rows, s) : launch<128, false>(m, p, a_rows, s);
   return glu ? launch<32, true>(m, p, a_rows, s) : launch<32, false>(m, p, a_rows, s);
 }
