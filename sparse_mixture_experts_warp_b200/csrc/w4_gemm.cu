@@ -10,8 +10,8 @@
 //   D[n, t] = sum_k w[n, k] a[row0 + t, k]       (TMEM lane = weight row, column = token)
 // so one thread owns one weight row: its codes, its group scales, its row factor, and its lane of
 // the A operand.  scale * (code - zero) is a bf16 exactly, so nothing is rounded on the way in.
-// A tile is 128 weight rows by up to NT tokens of one group; N of the MMA is the token count
-// rounded up to 16.  SwiGLU: lanes 0..15 of every 32 hold 16 rows of W_gate, lanes 16..31 the
+// A tile is 128 weight rows by up to NT tokens of one group (a group's tiles alike); N of the MMA
+// is the token count rounded up to 16.  SwiGLU: lanes 0..15 of every 32 hold 16 rows of W_gate, lanes 16..31 the
 // same rows of W_up, so gate and up of a feature are one warp shuffle apart.
 //
 // Roles (one persistent CTA per SM; tiles group by group, weight tile by weight tile, token tiles
@@ -19,16 +19,19 @@
 //   warp 0       TMA producer of the weights: 256 k of codes (128 rows x 128 bytes, 128-byte
 //                swizzle: a thread's 16-byte reads of its row are free of bank conflicts), and
 //                their scales and zero points, per stage;
-//   warp 1       TMA producer of the token rows: 64 k (NT = 256) to 256 k (NT = 32) per stage, in
-//                boxes of 64 k (128-byte swizzle);
+//   warp 1       TMA producer of the token rows: 64 k (NT = 192) to 256 k (NT = 32) per stage, in
+//                boxes of 64 k (128-byte swizzle) by the whole tile's rows, or by 64 of them where
+//                fewer do (up, Mixtral width, 2048 tokens: 989 us with boxes of 32 rows, 926 with
+//                64, 897 with 192);
 //   warp 2       MMA issuer (tcgen05.mma kind::f16, A from tensor memory) and TMEM owner;
 //   warp 3       group table;
-//   warps 4..    dequantisers: 4 * DQ warps, each set of four takes every DQ-th
+//   warps 4..    dequantisers: DQ sets of four warps, each takes every DQ-th
 //                128-element k-block, thread by thread 16 words -> 64 columns of packed bf16
-//                pairs (tcgen05.st), into a ring of 4 A stages of 64 columns;
+//                pairs (tcgen05.st), into the ring of A stages of 64 columns;
 //   then         epilogue: tcgen05.ld, row factor, activation, bf16 stores.
-// TMEM: 256 accumulator columns (one tile of up to 256 tokens, or two of up to 128 so that the
-// epilogue of a tile overlaps the next one's main loop) and 4 x 64 columns of A.
+// TMEM: two accumulators, so that the epilogue of a tile overlaps the next one's main loop, and a
+// ring of A stages: 2 x 192 and 2 x 64 columns, or 2 x 128 and 4 x 64.  (One accumulator of 256
+// columns left the tensor pipe idle for as long as an epilogue takes, a quarter of the time.)
 // When few tokens share a weight the loop has to run at the rate of the weights' bytes (a stage
 // of 16 KB of codes every 0.4 us), so stages are as long as memory allows: at 64-element A and
 // token stages the barrier traffic of the one MMA thread alone took 1.2 us for 16 KB.
@@ -170,7 +173,8 @@ __device__ __forceinline__ void dequant_word(uint32_t w, __nv_bfloat162 z, __nv_
 
 template <int NT, bool GLU>
 __global__ void __launch_bounds__(w4_threads<NT>(), 1)
-w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmC0,
+w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXall,
+               const __grid_constant__ CUtensorMap tmC0,
                const __grid_constant__ CUtensorMap tmC1, const __grid_constant__ CUtensorMap tmS0,
                const __grid_constant__ CUtensorMap tmS1, const __grid_constant__ CUtensorMap tmZ0,
                const __grid_constant__ CUtensorMap tmZ1, const W4Params p) {
@@ -330,6 +334,7 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
       const W4Tile tl = w4_locate<NT>(t, grp_off, tile_pre, g);
       const int nbox = (tl.ntok + XBOX - 1) / XBOX;
+      const bool all = nbox * XBOX == NT;       // as many rows as a box of the whole tile has
       for (int kb = 0; kb < nkb; kb += XB) {
         if (!wait(x_empty + 8 * stage, phase ^ 1u, DEVERR_TIMEOUT_TMA)) {
           ok = false;
@@ -339,10 +344,14 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         const int here = min(XB, nkb - kb);
         if (leader) {
           bar_expect(bar, here * nbox * XBOX_BYTES);
-          for (int h = 0; h < here; ++h)
-            for (int b = 0; b < nbox; ++b)
-              bar_load(xs + stage * X_STAGE + h * X_BOX + b * XBOX_BYTES, &tmX, bar,
-                       (kb + h) * W4_KB, tl.row0 + b * XBOX);
+          for (int h = 0; h < here; ++h) {
+            const uint32_t to = xs + stage * X_STAGE + h * X_BOX;
+            if (all)
+              bar_load(to, &tmXall, bar, (kb + h) * W4_KB, tl.row0);
+            else
+              for (int b = 0; b < nbox; ++b)
+                bar_load(to + b * XBOX_BYTES, &tmX, bar, (kb + h) * W4_KB, tl.row0 + b * XBOX);
+          }
         }
         issued |= 1u << stage;
         issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
@@ -572,7 +581,7 @@ size_t w4_smem(int G) {
 }
 
 struct W4Maps {
-  CUtensorMap x, c0, c1, s0, s1, z0, z1;
+  CUtensorMap x, xall, c0, c1, s0, s1, z0, z1;
 };
 
 template <int NT, bool GLU>
@@ -585,7 +594,7 @@ cudaError_t launch(const W4Maps& m, const W4Params& p, int64_t a_rows, cudaStrea
   const int64_t most = ((a_rows + NT - 1) / NT + p.G) * (int64_t)p.nt;
   const int sms = gemm_sm_count();
   const int grid = (int)(most < sms ? most : sms);
-  return launch_pdl(kern, dim3(grid), dim3(w4_threads<NT>()), smem, s, m.x, m.c0, m.c1, m.s0, m.s1, m.z0,
+  return launch_pdl(kern, dim3(grid), dim3(w4_threads<NT>()), smem, s, m.x, m.xall, m.c0, m.c1, m.s0, m.s1, m.z0,
                     m.z1, p);
 }
 
@@ -614,6 +623,7 @@ cudaError_t launch_w4_gemm(int act, const void* a, int64_t a_rows, int K, const 
                        feats, false);
   };
   if (!make_map(&m.x, a, (uint64_t)a_rows, (uint64_t)K, xbox, W4_KB) ||
+      !make_map(&m.xall, a, (uint64_t)a_rows, (uint64_t)K, nt_tok, W4_KB) ||
       !maps(w, &m.c0, &m.s0, &m.z0) || !maps(glu ? gate : w, &m.c1, &m.s1, &m.z1))
     return cudaErrorInvalidValue;
   W4Params p{};
