@@ -610,8 +610,12 @@ cudaError_t launch_w4_gemm(int act, const void* a, int64_t a_rows, int K, const 
     return cudaErrorInvalidValue;
   const bool glu = gate != nullptr;
   const int feats = glu ? 64 : 128;
+  // Tokens per tile by the groups' mean rows; groups differ, so a tile holds more than the mean.
+  // Tiles of 32 / 128 / 192 tokens, us: 8 groups of 14336 x 4096, gate and up, 16 rows a group
+  // 199 / 205 / 227, 32 rows 271 / 208 / 230, 64 rows 453 / 210 / 265, 128 rows 830 / 332 / 277;
+  // 32 uneven groups of 2048 x 7168, 7 rows 187 / 194 / 215, 15 rows 214 / 195 / 216.
   const int64_t mean = (a_rows + G - 1) / G;
-  const int nt_tok = mean > 128 ? 192 : mean > 24 ? 128 : 32;
+  const int nt_tok = mean > 96 ? 192 : mean > 12 ? 128 : 32;
   const int xbox = nt_tok == 32 ? W4Shape<32>::XBOX : W4Shape<128>::XBOX;
   alignas(64) W4Maps m;
   auto maps = [&](const moe_w4_t* q, CUtensorMap* c, CUtensorMap* sc, CUtensorMap* z) {
