@@ -522,8 +522,8 @@ moe_status_t moe_get_device_error(moe_stream_t stream, int32_t* code);
 int64_t moe_kernel_launches(void);
 
 /* Test hook for the bounded device waits (failure detection without a GPU fault).  fault = 1:
- * in every following bf16 expert projection, CTA 0 of the grouped GEMM arms its first ring
- * stage without loading it, so the MMA issuer's bounded wait runs out (about 2 s); the CTA
+ * in every following bf16 or 4-bit expert projection, CTA 0 of the product arms its first ring
+ * stage without loading it, so the bounded wait for it runs out (about 2 s); the CTA
  * records MOE_ERR_TIMEOUT in the device error word, drains what is in flight, frees its tensor
  * memory and exits, the other CTAs finish, and the context stays usable.  fault = 0 restores
  * normal operation.  Not for production use: the affected call's outputs are incomplete.

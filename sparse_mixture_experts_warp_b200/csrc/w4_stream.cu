@@ -238,7 +238,10 @@ w4_stream_kernel(const __grid_constant__ StreamMaps m0, const __grid_constant__ 
     for (int t = t_lo; t < t_hi && ok; ++t) {
       const int row = tl.g * p.N + tl.n0;
       for (int s0 = 0; s0 < nst; s0 += p.WK) {
-        if (!wait(empty + 8 * slot, phase ^ 1u, DEVERR_TIMEOUT_TMA)) {
+        // Warps that gave up on a stage go on to release it, with the flag raised before: no stage
+        // is armed again whose copies never came.
+        if (!wait(empty + 8 * slot, phase ^ 1u, DEVERR_TIMEOUT_TMA) ||
+            __any_sync(kFullWarp, *abort_flag)) {
           ok = false;
           break;
         }
