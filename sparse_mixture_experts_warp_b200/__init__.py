@@ -473,7 +473,7 @@ class W4:
 
     codes [G, N, K / 2] uint8, scales [G, ceil(K / group), N] float8_e4m3fn, zeros (uint8, the
     shape of scales) or None, row_scale [G, N] fp32; contiguous, on one device.  A single matrix
-    may leave G out."""
+    may leave G out.  The attributes are fixed: other tensors make another W4."""
 
     def __init__(self, codes, scales, zeros, row_scale, group):
         if codes.dim() not in (2, 3) or codes.dtype != torch.uint8:
@@ -490,9 +490,21 @@ class W4:
             raise ValueError(f"row_scale must be float32 {[*lead, N]}")
         if len({t.device for t in (codes, scales, zeros, row_scale) if t is not None}) > 1:
             raise ValueError("the tensors of 4-bit weights must be on one device")
-        self.codes, self.scales, self.zeros, self.row_scale = codes, scales, zeros, row_scale
-        self.group, self.G, self.N, self.K = group, lead[0] if lead else 1, N, K
-        self._c = MoeW4(_ptr(codes), _ptr(scales), _ptr(zeros), _ptr(row_scale), group, 0)
+        self.__dict__.update(
+            codes=codes, scales=scales, zeros=zeros, row_scale=row_scale, group=group,
+            G=lead[0] if lead else 1, N=N, K=K,
+            _c=MoeW4(_ptr(codes), _ptr(scales), _ptr(zeros), _ptr(row_scale), group, 0))
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"the {name} of 4-bit weights is fixed; make another W4")
+
+    def _ref(self):
+        """The C struct, with the addresses that the tensors have now."""
+        c = self._c
+        c.codes, c.scales = self.codes.data_ptr(), self.scales.data_ptr()
+        c.zeros = self.zeros.data_ptr() if self.zeros is not None else None
+        c.row_scale = self.row_scale.data_ptr()
+        return ctypes.byref(c)
 
 
 def empty_w4(G, N, K, group=128, zeros=False, device="cuda") -> W4:
@@ -510,7 +522,7 @@ def _w4(w, G, N, K, what):
     if (w.G, w.N, w.K) != (G, N, K):
         raise ValueError(f"{what} holds [{w.G}, {w.N}, {w.K}], not [{G}, {N}, {K}]")
     _here(w.codes)
-    return ctypes.byref(w._c)
+    return w._ref()
 
 
 def _w4_wide(W, w):
@@ -526,7 +538,7 @@ def moe_quantize_w4(W, w, stream=None):
     dt = _w4_wide(W, w)
     _here(W, w.codes)
     _check("moe_quantize_w4", lib().moe_quantize_w4(
-        w.G, w.N, w.K, dt, _ptr(W), ctypes.byref(w._c), _stream(stream)))
+        w.G, w.N, w.K, dt, _ptr(W), w._ref(), _stream(stream)))
 
 
 def moe_dequantize_w4(w, W, stream=None):
@@ -534,7 +546,7 @@ def moe_dequantize_w4(w, W, stream=None):
     dt = _w4_wide(W, w)
     _here(W, w.codes)
     _check("moe_dequantize_w4", lib().moe_dequantize_w4(
-        w.G, w.N, w.K, ctypes.byref(w._c), dt, _ptr(W), _stream(stream)))
+        w.G, w.N, w.K, w._ref(), dt, _ptr(W), _stream(stream)))
 
 
 def moe_expert_up_w4(d, n_groups, F, a, offsets, gate, up, h, stream=None):

@@ -176,6 +176,19 @@ def test_binding_checks_shapes():
         M.moe_expert_down_w4(d, 8, 512, rows, off, w, rows)
 
 
+def test_a_w4_keeps_to_its_tensors():
+    """Other tensors need another W4, and the addresses handed on are the tensors' present ones."""
+    w = M.empty_w4(2, 64, 192, 64, True, device="cpu")
+    for name in ("codes", "scales", "zeros", "row_scale", "group", "N"):
+        with pytest.raises(AttributeError):
+            setattr(w, name, getattr(w, name))
+    moved = [torch.zeros_like(t) for t in (w.codes, w.scales, w.zeros, w.row_scale)]
+    for t, m in zip((w.codes, w.scales, w.zeros, w.row_scale), moved):
+        t.data = m
+    c = w._ref()._obj
+    assert [c.codes, c.scales, c.zeros, c.row_scale] == [m.data_ptr() for m in moved]
+
+
 def test_bad_gradient_arguments_are_refused():
     L, n0 = M.lib(), M.kernel_launches()
     d = _desc()
