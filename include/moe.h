@@ -463,7 +463,8 @@ moe_status_t moe_dequantize_w4(int32_t n_matrices, int32_t N, int32_t K, const m
  * GELU; under SwiGLU of the same group and both with or both without zeros), down
  * [n_groups, D, F].  a, h, y bf16 (MOE_ERR_UNSUPPORTED for fp32 layers), fp32 sums; the other
  * arguments and the rows written are those of moe_expert_up / moe_expert_down, and results are
- * those of the values the weights stand for.  No scratch. */
+ * those of the values the weights stand for, but that a row's elements may enter with an error of
+ * up to 2^-39 of its largest one.  No scratch. */
 moe_status_t moe_expert_up_w4(const moe_desc_t* desc, int32_t n_groups, int32_t F,
                               const void* a, int64_t a_rows, const int32_t* offsets,
                               const moe_w4_t* gate, const moe_w4_t* up, void* h,

@@ -60,8 +60,8 @@ template <> struct Vec<false> {
 };
 
 // y and dy may be the same rows (a lane reads its vectors before it writes them), so neither is
-// __restrict__.  W warps take one token; a block of 8 warps 8 / W tokens.  Rows longer than W * kSpan vectors
-// go in passes, whose dots add up in shared memory (each cell has one owner: no atomics).
+// __restrict__.  W warps take one token; a block of 8 warps 8 / W tokens.  Rows longer than
+// W * kSpan vectors go in passes, whose dots add up in shared memory (each cell has one owner: no atomics).
 template <bool BF16>
 __global__ void __launch_bounds__(kWarps * 32)
 combine_backward_kernel(const uint4* __restrict__ dout, const uint4* y,

@@ -5,8 +5,9 @@
 // with 4-bit codes, e4m3 scales per group of g = 32, 64 or 128 consecutive k, 4-bit zero points
 // (8 everywhere when absent) and one fp32 factor per row.  code - zero has at most 4 significant
 // bits and so has an e4m3 number: the product in the inner brackets has at most 8 and is a bf16
-// exactly.  The tensor cores therefore take scale * (code - zero) as their bf16 operand without
-// any rounding, and row_scale is one fp32 factor on the finished sum.  Scales and zero points
+// exactly.  The tensor cores therefore take scale * (code - zero) as their bf16 operand (or, for
+// few rows, code - zero as their fp16 operand and scale on the group's fp32 sum) without any
+// rounding, and row_scale is one fp32 factor on the finished sum.  Scales and zero points
 // are stored [K / g, N] (rows of a tile are neighbours in memory).
 //
 // Codes: 64 consecutive k of a row are 32 bytes, eight little-endian words; word 2 c + j holds

@@ -11,8 +11,8 @@
 // so one thread owns one weight row: its codes, its group scales, its row factor, and its lane of
 // the A operand.  scale * (code - zero) is a bf16 exactly, so nothing is rounded on the way in.
 // A tile is 128 weight rows by up to NT tokens of one group (a group's tiles alike); N of the MMA
-// is the token count rounded up to 16.  SwiGLU: lanes 0..15 of every 32 hold 16 rows of W_gate, lanes 16..31 the
-// same rows of W_up, so gate and up of a feature are one warp shuffle apart.
+// is the token count rounded up to 16.  SwiGLU: lanes 0..15 of every 32 hold 16 rows of W_gate,
+// lanes 16..31 the same rows of W_up, so gate and up of a feature are one warp shuffle apart.
 //
 // Roles (one persistent CTA per SM; tiles group by group, weight tile by weight tile, token tiles
 // innermost, so that the CTAs that run together share weight tiles through L2):
@@ -35,6 +35,14 @@
 // When few tokens share a weight the loop has to run at the rate of the weights' bytes (a stage
 // of 16 KB of codes every 0.4 us), so stages are as long as memory allows: at 64-element A and
 // token stages the barrier traffic of the one MMA thread alone took 1.2 us for 16 KB.
+// What bounds it (8 groups of 14336 x 4096, gate and up): at 256 rows a group and more the pace of
+// the dequantisers and the MMAs together (2048 tokens: 854 us, 1.13 PFLOP/s; 697 with the
+// dequantising arithmetic left out, 533 with the MMAs left out too), under the power cap.  At 8 to
+// 64 rows a group about 200 us (2.4 TB/s of codes): 164 to 194 without arithmetic and MMAs, so the
+// hand-over from stage to stage.  Twice the dequantisers (two warps a row, half an A stage each)
+// made 2048 tokens 10% slower, a rolled loop over an A stage's halves 15%, all eight MMAs of a
+// stage behind one branch 15%, predicated MMAs 5%; token boxes of exactly the tile's rows changed
+// nothing at 6 rows and cost 20% at 512.
 // Every mbarrier wait is bounded (globaltimer); a wait that gives up records an error code in
 // the device error word and the CTA drains what it has in flight and exits.
 #include <cuda.h>
@@ -76,7 +84,8 @@ template <> struct W4Shape<32> {
 template <int NT> constexpr int w4_threads() {
   using S = W4Shape<NT>;
   static_assert(S::AS % S::DQ == 0, "an A stage has one set of dequantisers");
-  static_assert(S::ACCS * (NT < 128 ? 128 : NT) + S::AS * W4_A_COLS <= W4_TMEM_COLS, "TMEM columns");
+  static_assert(S::ACCS * (NT < 128 ? 128 : NT) + S::AS * W4_A_COLS <= W4_TMEM_COLS,
+                "TMEM columns");
   return 32 * (W4_FIRST_DQ + 4 * S::DQ + 4 * S::EPI);
 }
 
@@ -594,8 +603,8 @@ cudaError_t launch(const W4Maps& m, const W4Params& p, int64_t a_rows, cudaStrea
   const int64_t most = ((a_rows + NT - 1) / NT + p.G) * (int64_t)p.nt;
   const int sms = gemm_sm_count();
   const int grid = (int)(most < sms ? most : sms);
-  return launch_pdl(kern, dim3(grid), dim3(w4_threads<NT>()), smem, s, m.x, m.xall, m.c0, m.c1, m.s0, m.s1, m.z0,
-                    m.z1, p);
+  return launch_pdl(kern, dim3(grid), dim3(w4_threads<NT>()), smem, s, m.x, m.xall, m.c0, m.c1,
+                    m.s0, m.s1, m.z0, m.z1, p);
 }
 
 }  // namespace

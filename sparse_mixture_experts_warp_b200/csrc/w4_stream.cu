@@ -14,7 +14,7 @@
 //     half word: one shift and four mask-and-or steps per 8 codes (bf16's 7 bits need three
 //     shifts).  A token row is scaled by the power of two that brings its largest element to
 //     [2^14, 2^15): its bf16 elements are then fp16 numbers exactly down to 2^-32 of the largest,
-//     and what lies below is off by less than 2^-40 of it, far under the fp32 sums' own rounding.
+//     and what lies below is off by at most 2^-39 of it, far under the fp32 sums' own rounding.
 //     The inverse power multiplies the finished sum.
 //
 // A CTA takes a tile of RT * 16 weight rows (SwiGLU: RT * 8 features, 8 rows of W_gate above the
