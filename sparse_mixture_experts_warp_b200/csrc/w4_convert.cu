@@ -19,6 +19,8 @@
 // memory (they are stored [group, row]: a row's own are N bytes apart).
 #include <float.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "w4.cuh"
 
@@ -98,9 +100,9 @@ template <> struct Eight<false> {
 constexpr int kMaxWarps = 16;
 template <bool BF16, bool ZEROS> constexpr int words_of() { return BF16 && !ZEROS ? 8 : 4; }
 
-template <bool BF16, bool ZEROS>
+template <bool BF16, bool ZEROS, int GROUP>
 __global__ void __launch_bounds__(32 * kMaxWarps)
-quantize_w4_kernel(const void* __restrict__ W, int N, int K, int g, int per_block,
+quantize_w4_kernel(const void* __restrict__ W, int N, int K, int per_block,
                    uint32_t* __restrict__ codes, uint8_t* __restrict__ scales,
                    uint8_t* __restrict__ zeros, float* __restrict__ row_scale) {
   constexpr int kWords = words_of<BF16, ZEROS>();
@@ -108,7 +110,8 @@ quantize_w4_kernel(const void* __restrict__ W, int N, int K, int g, int per_bloc
   __shared__ float s_max[2][kMaxWarps];
   pdl_trigger();
   pdl_wait();
-  const int words = K / 8, gw = g / 8, groups = (K + g - 1) / g;
+  constexpr int gw = GROUP / 8;                 // words of a group
+  const int words = K / 8, groups = (K + GROUP - 1) / GROUP;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int64_t row0 = (int64_t)blockIdx.x * per_block;         // matrix * N + n
   const int64_t m = row0 / N;
@@ -117,7 +120,7 @@ quantize_w4_kernel(const void* __restrict__ W, int N, int K, int g, int per_bloc
   // The kWords words of a lane are of as many groups, the same for the gw lanes of a group: lane
   // `sub` of them does the divisions for word `sub` (of 8 words, gw = 4: and for word 4 + sub).
   const int sub = lane & (gw - 1), pick = sub & (kWords - 1);
-  const bool twice = gw < kWords;
+  constexpr bool twice = gw < kWords;
   Eight<BF16> e[kWords];
   float raw[kWords], lo[kWords];                // a word's group: range, smallest weight (or 0)
   auto fetch = [&](int64_t row, int base) {
@@ -133,6 +136,7 @@ quantize_w4_kernel(const void* __restrict__ W, int N, int K, int g, int per_bloc
     for (int r = 0; r < kWords; ++r) {
       float hi;
       e[r].template range<ZEROS>(hi, lo[r]);
+#pragma unroll
       for (int o = 1; o < gw; o <<= 1) {
         hi = max_nan(hi, __shfl_xor_sync(kFull, hi, o));
         if (ZEROS) lo[r] = min_nan(lo[r], __shfl_xor_sync(kFull, lo[r], o));
@@ -336,15 +340,22 @@ cudaError_t launch_quantize_w4(int n_matrices, int N, int K, bool bf16, const vo
   const size_t side = (size_t)groups * (o.zeros ? 2 : 1);
   while (per > 4 && (rows / per < (int64_t)num_sms() * 16 || side * per > 40960)) per /= 2;
   const size_t smem = side * per;
-  auto k = bf16 ? (o.zeros ? quantize_w4_kernel<true, true> : quantize_w4_kernel<true, false>)
-                : (o.zeros ? quantize_w4_kernel<false, true> : quantize_w4_kernel<false, false>);
-  if (smem > 40960) {
-    cudaError_t e =
-        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_pdl(k, dim3((unsigned)(rows / per)), dim3(32 * warps), smem, s, W, N, K, o.group,
-                    per, reinterpret_cast<uint32_t*>(o.codes), o.scales, o.zeros, o.row_scale);
+  auto run = [&](auto group) {
+    constexpr int G = decltype(group)::value;
+    auto k = bf16 ? (o.zeros ? quantize_w4_kernel<true, true, G> : quantize_w4_kernel<true, false, G>)
+                  : (o.zeros ? quantize_w4_kernel<false, true, G>
+                             : quantize_w4_kernel<false, false, G>);
+    if (smem > 40960) {
+      cudaError_t e =
+          cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(k, dim3((unsigned)(rows / per)), dim3(32 * warps), smem, s, W, N, K, per,
+                      reinterpret_cast<uint32_t*>(o.codes), o.scales, o.zeros, o.row_scale);
+  };
+  if (o.group == 32) return run(std::integral_constant<int, 32>{});
+  if (o.group == 64) return run(std::integral_constant<int, 64>{});
+  return run(std::integral_constant<int, 128>{});
 }
 
 cudaError_t launch_dequantize_w4(int n_matrices, int N, int K, const moe_w4_t& w, bool bf16,
