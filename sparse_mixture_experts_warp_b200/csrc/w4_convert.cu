@@ -95,17 +95,13 @@ template <> struct Eight<false> {
 // warps: a thread holds kWords runs of eight consecutive k (one word of codes each), so the g / 8
 // threads of a group are neighbouring lanes.  Rows longer than the largest block holds are read
 // again for their codes.
-// kWords = 8 where a lane's registers allow it (bf16 without zero points: 293 instead of 365 us for
-// 8 x 4096 x 14336; fp32 rows took 432 instead of 346 us for want of occupancy), else 4.
-constexpr int kMaxWarps = 16;
-template <bool BF16, bool ZEROS> constexpr int words_of() { return BF16 && !ZEROS ? 8 : 4; }
+constexpr int kMaxWarps = 16, kWords = 4;
 
 template <bool BF16, bool ZEROS, int GROUP>
 __global__ void __launch_bounds__(32 * kMaxWarps)
 quantize_w4_kernel(const void* __restrict__ W, int N, int K, int per_block,
                    uint32_t* __restrict__ codes, uint8_t* __restrict__ scales,
                    uint8_t* __restrict__ zeros, float* __restrict__ row_scale) {
-  constexpr int kWords = words_of<BF16, ZEROS>();
   extern __shared__ __align__(16) uint8_t s_side[];             // [groups][per_block] scales, zeros
   __shared__ float s_max[2][kMaxWarps];
   pdl_trigger();
@@ -117,18 +113,24 @@ quantize_w4_kernel(const void* __restrict__ W, int N, int K, int per_block,
   const int64_t m = row0 / N;
   const int n0 = (int)(row0 - m * N);
   uint8_t* s_zero = s_side + groups * per_block;
-  // The kWords words of a lane are of as many groups, the same for the gw lanes of a group: lane
-  // `sub` of them does the divisions for word `sub` (of 8 words, gw = 4: and for word 4 + sub).
-  const int sub = lane & (gw - 1), pick = sub & (kWords - 1);
-  constexpr bool twice = gw < kWords;
+  // The kWords words of a lane are of as many groups, the same for the gw >= kWords lanes of a
+  // group: lane `sub` of them does the divisions for word `sub`.
+  static_assert(gw >= kWords, "a lane per word");
+  const int sub = lane & (gw - 1), mine = sub & (kWords - 1);
   Eight<BF16> e[kWords];
   float raw[kWords], lo[kWords];                // a word's group: range, smallest weight (or 0)
   auto fetch = [&](int64_t row, int base) {
+    const int i = base + warp * 32 + lane, step = warps * 32;
+    const int64_t at = row * words + i;
+    if (base + kWords * step <= words) {
 #pragma unroll
-    for (int r = 0; r < kWords; ++r) {
-      const int i = base + (r * warps + warp) * 32 + lane;
-      e[r].zero();
-      if (i < words) e[r].load(W, row * words + i);
+      for (int r = 0; r < kWords; ++r) e[r].load(W, at + r * step);
+    } else {
+#pragma unroll
+      for (int r = 0; r < kWords; ++r) {
+        e[r].zero();
+        if (i + r * step < words) e[r].load(W, at + r * step);
+      }
     }
   };
   auto ranges = [&]() {
@@ -172,44 +174,36 @@ quantize_w4_kernel(const void* __restrict__ W, int N, int K, int per_block,
         fetch(row, base);
         ranges();
       }
-      float my_inv[2];
-      int my_zero[2] = {8, 8};
-      bool clamp = false;
+      float my_raw = raw[0], my_lo = lo[0];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (h && !twice) break;
-        const int mine = pick + 4 * h;
-        float my_raw = raw[0], my_lo = lo[0];
-#pragma unroll
-        for (int r = 1; r < kWords; ++r)
-          if (mine == r) {
-            my_raw = raw[r];
-            my_lo = lo[r];
-          }
-        const float t = __fdiv_rn(my_raw, kSpread);
-        const __nv_fp8_e4m3 sc(rs > 0.f ? __fdiv_rn(t, rs) : 0.f);
-        const float step = static_cast<float>(sc) * rs;
-        my_inv[h] = step > 0.f ? __fdiv_rn(1.f, step) : 0.f;
-        if (ZEROS) my_zero[h] = (int)fminf(fmaxf(rintf(-my_lo * my_inv[h]), 0.f), 15.f);
-        // a scale that is a normal e4m3 (from 2^-6 on, byte 8) is off by at most a 16th, so |w r|
-        // is below 7.5 and its rounding needs no clamp; nor where the codes do not matter (r = 0),
-        // but an infinity or a NaN has to stay in its nibble
-        clamp |= !(my_raw <= FLT_MAX) || (sc.__x < 8 && my_inv[h] > 0.f);
-        const int at = base + (mine * warps + warp) * 32 + lane;  // a word of that group
-        if (sub < kWords && at < words) {
-          s_side[at / gw * per_block + j] = sc.__x;
-          if (ZEROS) s_zero[at / gw * per_block + j] = (uint8_t)my_zero[h];
+      for (int r = 1; r < kWords; ++r)
+        if (mine == r) {
+          my_raw = raw[r];
+          my_lo = lo[r];
         }
+      const float t = __fdiv_rn(my_raw, kSpread);
+      const __nv_fp8_e4m3 sc(rs > 0.f ? __fdiv_rn(t, rs) : 0.f);
+      const float step = static_cast<float>(sc) * rs;
+      const float my_inv = step > 0.f ? __fdiv_rn(1.f, step) : 0.f;
+      const int my_zero = ZEROS ? (int)fminf(fmaxf(rintf(-my_lo * my_inv), 0.f), 15.f) : 8;
+      // a scale that is a normal e4m3 (from 2^-6 on, byte 8) is off by at most a 16th, so |w r|
+      // is below 7.5 and its rounding needs no clamp; nor where the codes do not matter (r = 0),
+      // but an infinity or a NaN has to stay in its nibble
+      bool clamp = !(my_raw <= FLT_MAX) || (sc.__x < 8 && my_inv > 0.f);
+      const int word0 = base + (mine * warps + warp) * 32 + lane;       // a word of that group
+      if (sub < kWords && word0 < words) {
+        s_side[word0 / gw * per_block + j] = sc.__x;
+        if (ZEROS) s_zero[word0 / gw * per_block + j] = (uint8_t)my_zero;
       }
       clamp = __any_sync(kFull, clamp);
+      // words of a block are 8 consecutive k each: k / 8 = 8 b + 4 j + c is word 8 b + 2 c + j
+      // (in the row or not with the rest of its block)
+      const int to = base + warp * 32 + (lane & ~7) + 2 * (lane & 3) + ((lane >> 2) & 1);
 #pragma unroll
       for (int r = 0; r < kWords; ++r) {
-        const int from = (lane & ~(gw - 1)) + (twice ? r & 3 : r);
-        const int h = twice ? r / 4 : 0;
-        const float inv = __shfl_sync(kFull, h ? my_inv[1] : my_inv[0], from);
-        const int zero = ZEROS ? __shfl_sync(kFull, h ? my_zero[1] : my_zero[0], from) : 8;
-        const int i = base + (r * warps + warp) * 32 + lane;
-        if (i >= words) continue;
+        const int from = (lane & ~(gw - 1)) + r;
+        const float inv = __shfl_sync(kFull, my_inv, from);
+        const int zero = ZEROS ? __shfl_sync(kFull, my_zero, from) : 8;
         // clamped, then rounded: the bounds are whole numbers, so the order does not matter; the
         // sum of the eight rounded ones' bits, 16^p times each, is the word plus a constant
         const float least = ZEROS ? -(float)zero : -8.f, largest = ZEROS ? 15.f - zero : 7.f;
@@ -228,9 +222,7 @@ quantize_w4_kernel(const void* __restrict__ W, int N, int K, int per_block,
         }
         // sum of kRoundBits 16^p (p = 0..7) is kRoundBits * 0x11111111, and each nibble gets zero
         word += (uint32_t)zero * 0x11111111u - kRoundBits * 0x11111111u;
-        // words of a block are 8 consecutive k each: k / 8 = 8 b + 4 j + c is word 8 b + 2 c + j
-        const int b = i >> 3, j2 = (i >> 2) & 1, c = i & 3;
-        codes[row * words + 8 * b + 2 * c + j2] = word;
+        if (to + r * 32 * warps < words) codes[row * words + to + r * 32 * warps] = word;
       }
     }
   }
@@ -331,7 +323,7 @@ cudaError_t launch_quantize_w4(int n_matrices, int N, int K, bool bf16, const vo
                                const moe_w4_t& o, cudaStream_t s) {
   const int64_t rows = (int64_t)n_matrices * N;
   const int words = K / 8, groups = (K + o.group - 1) / o.group;
-  const int each = 32 * (bf16 && !o.zeros ? words_of<true, false>() : words_of<false, false>());
+  const int each = 32 * kWords;
   int warps = (words + each - 1) / each;
   if (warps > kMaxWarps) warps = kMaxWarps;
   // rows per block: 32 fill a sector of scales; fewer when the blocks would not fill the SMs a
