@@ -55,6 +55,20 @@ def test_quantize_and_dequantize(G, N, K, group, zeros, dtype):
     assert torch.equal(b, f.to(torch.bfloat16))
 
 
+@pytest.mark.parametrize("G,N,K,group,zeros,dtype", [
+    (3, 6400, 192, 64, True, torch.bfloat16),       # blocks of 8 rows, one after the other
+    (3, 6400, 2048, 128, False, torch.bfloat16),
+    (10, 7616, 128, 32, False, torch.float32),      # of 32 rows
+    (10, 7616, 192, 128, True, torch.float32),      # (and a short group)
+    (10, 7616, 576, 32, True, torch.bfloat16),
+    (1, 64, 4096, 64, False, torch.bfloat16),       # of 4 rows, 4 at a time, 2 or one
+    (1, 64, 6464, 64, True, torch.float32),
+    (1, 64, 9152, 128, True, torch.bfloat16),
+])
+def test_rows_per_block(G, N, K, group, zeros, dtype):
+    test_quantize_and_dequantize(G, N, K, group, zeros, dtype)
+
+
 def test_nonfinite_rows_stand_for_nan():
     X = torch.randn(1, 64, 256, device="cuda")
     X[0, 1, 7] = float("nan")
