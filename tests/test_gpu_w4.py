@@ -69,6 +69,18 @@ def test_rows_per_block(G, N, K, group, zeros, dtype):
     test_quantize_and_dequantize(G, N, K, group, zeros, dtype)
 
 
+@pytest.mark.parametrize("dtype,skip", [(torch.float32, 4), (torch.bfloat16, 8)])
+def test_dequantize_to_16_byte_alignment(dtype, skip):
+    w = W.random_w4(2, 64, 192, 64, True, 4)
+    a = torch.empty(2, 64, 192, dtype=dtype, device="cuda")
+    M.moe_dequantize_w4(w, a)
+    room = torch.full((skip + a.numel() + skip,), 7.0, dtype=dtype, device="cuda")
+    b = room[skip:-skip].view(a.shape)
+    M.moe_dequantize_w4(w, b)
+    assert torch.equal(a, b)
+    assert (room[:skip] == 7).all() and (room[-skip:] == 7).all()
+
+
 def test_nonfinite_rows_stand_for_nan():
     X = torch.randn(1, 64, 256, device="cuda")
     X[0, 1, 7] = float("nan")
