@@ -1,5 +1,6 @@
 /*
- * moe.h -- C ABI of the B200 (sm_100a) sparse Mixture-of-Experts FFN layer, forward pass.
+ * moe.h -- C ABI of the B200 (sm_100a) sparse Mixture-of-Experts FFN layer: forward, backward, and
+ * the products of 4-bit expert weights.
  *
  * The layer, as the pages define it (Gate -> Dispatch -> Expert compute -> Combine):
  *   "Top-k 路由（Top-k Routing）" (compassingai), "Top-k 路由的完整生命週期" and

@@ -36,10 +36,11 @@
 // of 16 KB of codes every 0.4 us), so stages are as long as memory allows: at 64-element A and
 // token stages the barrier traffic of the one MMA thread alone took 1.2 us for 16 KB.
 // What bounds it (8 groups of 14336 x 4096, gate and up): at 256 rows a group and more the pace of
-// the dequantisers and the MMAs together (2048 tokens: 854 us, 1.13 PFLOP/s; 697 with the
-// dequantising arithmetic left out, 533 with the MMAs left out too), under the power cap.  At 8 to
-// 64 rows a group about 200 us (2.4 TB/s of codes): 164 to 194 without arithmetic and MMAs, so the
-// hand-over from stage to stage.  Twice the dequantisers (two warps a row, half an A stage each)
+// the dequantisers and the MMAs together (2048 tokens: 816 to 847 us, 1.14 to 1.18 PFLOP/s under
+// the power cap, the tensor pipe 81% busy in the 703 us that one launch takes at full clock; before
+// the pairs' mask and magic became one step 818 us, of which 697 were left without the dequantising
+// arithmetic and 533 without the MMAs too).  At 8 to 64 rows a group about 200 us (2.4 TB/s of
+// codes): 164 to 194 without arithmetic and MMAs, so the hand-over from stage to stage.  Twice the dequantisers (two warps a row, half an A stage each)
 // made 2048 tokens 10% slower, a rolled loop over an A stage's halves 15%, all eight MMAs of a
 // stage behind one branch 15%, predicated MMAs 5%; token boxes of exactly the tile's rows changed
 // nothing at 6 rows and cost 20% at 512.
