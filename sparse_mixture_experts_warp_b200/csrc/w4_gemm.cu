@@ -40,10 +40,11 @@
 // the power cap, the tensor pipe 81% busy in the 703 us that one launch takes at full clock; before
 // the pairs' mask and magic became one step 818 us, of which 697 were left without the dequantising
 // arithmetic and 533 without the MMAs too).  At 8 to 64 rows a group about 200 us (2.4 TB/s of
-// codes): 164 to 194 without arithmetic and MMAs, so the hand-over from stage to stage.  Twice the dequantisers (two warps a row, half an A stage each)
-// made 2048 tokens 10% slower, a rolled loop over an A stage's halves 15%, all eight MMAs of a
-// stage behind one branch 15%, predicated MMAs 5%; token boxes of exactly the tile's rows changed
-// nothing at 6 rows and cost 20% at 512.
+// codes): 164 to 194 without arithmetic and MMAs, so the hand-over from stage to stage.  Twice the
+// dequantisers (two warps a row, half an A stage each) made 2048 tokens 13% slower, a rolled loop
+// over an A stage's halves 15%, all eight MMAs of a stage behind one branch 27%, predicated MMAs
+// 7%; token boxes of exactly the tile's rows changed nothing at 12 rows a group and cost a third at
+// 512.
 // Every mbarrier wait is bounded (globaltimer); a wait that gives up records an error code in
 // the device error word and the CTA drains what it has in flight and exits.
 #include <cuda.h>

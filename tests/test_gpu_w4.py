@@ -178,6 +178,13 @@ def test_many_groups(op):
 
 
 @pytest.mark.parametrize("op", ["up", "down"])
+@pytest.mark.parametrize("rows", [1, 20, 100])
+def test_most_groups(op, rows):
+    """1024 groups, the most a call takes, on each kernel and its largest tiles."""
+    _run([rows] * 1023 + [0], 64, 64, "relu", 64, True, op=op)
+
+
+@pytest.mark.parametrize("op", ["up", "down"])
 @pytest.mark.parametrize("counts", [[2, 3], [70, 30]])
 def test_groups_that_start_behind_row_zero(op, counts):
     _run(counts, 192, 256, "relu", 64, False, op=op, first=5)
