@@ -70,23 +70,24 @@ constexpr int W4_TMEM_COLS = 512;
 constexpr int W4_FIRST_DQ = 4;
 
 // Tokens of a tile; weight stages; token stages, their k and the rows of their boxes; accumulators;
-// A stages; sets of four dequantisers and of four epilogue warps.  A stage of the A ring belongs
-// to one set of dequantisers: another set could be two rounds ahead of it and take the wait's
-// parity for its own.
+// sets of four dequantisers and of four epilogue warps.  A weight stage of 256 k has two A blocks
+// of 128: set i takes block i % 2 of every weight stage, or with four sets of every second one, and
+// has an A stage of its own.  So a stage of either ring belongs to the same sets every round;
+// others could be two rounds ahead and take a wait's parity for their own.
 template <int NT> struct W4Shape;
 template <> struct W4Shape<192> {
-  static constexpr int WS = 3, XS = 6, XK = 64, XBOX = 64, ACCS = 2, AS = 2, DQ = 2, EPI = 2;
+  static constexpr int WS = 3, XS = 6, XK = 64, XBOX = 64, ACCS = 2, DQ = 2, EPI = 2;
 };
 template <> struct W4Shape<128> {
-  static constexpr int WS = 5, XS = 3, XK = 128, XBOX = 64, ACCS = 2, AS = 4, DQ = 4, EPI = 1;
+  static constexpr int WS = 6, XS = 3, XK = 128, XBOX = 64, ACCS = 2, DQ = 4, EPI = 1;
 };
 template <> struct W4Shape<32> {
-  static constexpr int WS = 8, XS = 4, XK = 256, XBOX = 32, ACCS = 2, AS = 4, DQ = 4, EPI = 1;
+  static constexpr int WS = 8, XS = 4, XK = 256, XBOX = 32, ACCS = 2, DQ = 4, EPI = 1;
 };
 template <int NT> constexpr int w4_threads() {
   using S = W4Shape<NT>;
-  static_assert(S::AS % S::DQ == 0, "an A stage has one set of dequantisers");
-  static_assert(S::ACCS * (NT < 128 ? 128 : NT) + S::AS * W4_A_COLS <= W4_TMEM_COLS,
+  static_assert(S::DQ == 2 || (S::DQ == 4 && S::WS % 2 == 0), "a weight stage has the same sets");
+  static_assert(S::ACCS * (NT < 128 ? 128 : NT) + S::DQ * W4_A_COLS <= W4_TMEM_COLS,
                 "TMEM columns");
   return 32 * (W4_FIRST_DQ + 4 * S::DQ + 4 * S::EPI);
 }
@@ -196,7 +197,7 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
                const __grid_constant__ CUtensorMap tmS1, const __grid_constant__ CUtensorMap tmZ0,
                const __grid_constant__ CUtensorMap tmZ1, const W4Params p) {
   constexpr int WS = W4Shape<NT>::WS, XS = W4Shape<NT>::XS, XK = W4Shape<NT>::XK,
-                ACCS = W4Shape<NT>::ACCS, AS = W4Shape<NT>::AS, DQ = W4Shape<NT>::DQ,
+                ACCS = W4Shape<NT>::ACCS, DQ = W4Shape<NT>::DQ, AS = DQ,
                 EPI = W4Shape<NT>::EPI, XBOX = W4Shape<NT>::XBOX;
   constexpr int ACC_PITCH = NT < 128 ? 128 : NT;      // columns between accumulators
   constexpr int A_COL = ACCS * ACC_PITCH;             // first column of the A ring
@@ -231,7 +232,7 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
       for (int i = 0; i < n; ++i) mbar_init(b++, count);
     };
     init(WS, 1);
-    init(WS, 4 * DQ);
+    init(WS, 8);                                // two sets
     init(2 * XS, 1);
     init(AS, 4);
     init(AS, 1);
@@ -398,7 +399,7 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         break;
       }
       tc_fence_after();
-      for (int kb = 0; kb < nkb && ok; kb += W4_KA / W4_KB) {
+      for (int kb = 0; kb < 4 * nws && ok; kb += W4_KA / W4_KB) {     // (both A blocks of the last)
         if (!wait(a_full + 8 * ast, aph, DEVERR_TIMEOUT_MMA)) {
           ok = false;
           break;
@@ -447,79 +448,77 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     const int pitch = GLU ? 64 : 128;
     const int shift = p.group == 32 ? 5 : p.group == 64 ? 6 : 7;
     const uint32_t trow = tmem_base + A_COL + ((uint32_t)(32 * q) << 16);
-    int wst = 0, ast = 0;
-    uint32_t wph = 0, aph = 1, turn = 0;        // turn: A stages before this one, over all tiles
+    const int b0 = (set & 1) * (W4_KA / W4_KB);         // first 64-element block of its A block
+    const uint32_t a_col = trow + set * W4_A_COLS;
+    int wst = 0;
+    uint32_t wph = 0, aph = 1, mine = DQ == 4 ? set >> 1 : 0;   // own weight stage: mine is 0
     bool ok = true;
     for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-      for (int s = 0; s < nws && ok; ++s) {
-        if (!wait(w_full + 8 * wst, wph, DEVERR_TIMEOUT_TMA)) {
-          ok = false;
-          break;
-        }
-        const uint8_t* st = ws + wst * W4_W_STAGE;
-        const uint8_t* sc = st + W4_CODE_BYTES + side;
-        const uint8_t* zp = sc + W4_SIDE_BYTES;
-        const int here = min(4, nkb - 4 * s);
-        for (int b0 = 0; b0 < here; b0 += W4_KA / W4_KB, ++turn) {
-          if (turn % DQ == set) {
-            // everything of the A stage's 128 k first: codes, scales, zero points (a block past K
-            // is read as zeros or the next matrix's scales, and no MMA takes it)
-            const uint8_t* src = st + row * 128;
-            uint4 c[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              c[i] = *reinterpret_cast<const uint4*>(src + (((2 * b0 + i) ^ (row & 7)) << 4));
-            __nv_bfloat162 s2[4], z2[4];        // per 32 k
-            const int at = ((W4_KB * b0) >> shift) * pitch;
-            s2[0] = scale_pair(sc[at]);
-            z2[0] = zero_pair(p.zeros ? zp[at] : 8u);
-            if (shift == 7) {
-              s2[1] = s2[2] = s2[3] = s2[0];
-              z2[1] = z2[2] = z2[3] = z2[0];
-            } else if (shift == 6) {
-              s2[1] = s2[0];
-              z2[1] = z2[0];
-              s2[2] = s2[3] = scale_pair(sc[at + pitch]);
-              z2[2] = z2[3] = zero_pair(p.zeros ? zp[at + pitch] : 8u);
-            } else {
-#pragma unroll
-              for (int i = 1; i < 4; ++i) {
-                s2[i] = scale_pair(sc[at + i * pitch]);
-                z2[i] = zero_pair(p.zeros ? zp[at + i * pitch] : 8u);
-              }
-            }
-#pragma unroll
-            for (int h = 0; h < W4_KA / W4_KB; ++h) {
-              const uint4 lo = c[2 * h], hi = c[2 * h + 1];
-              const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-              uint32_t r[32];
-#pragma unroll
-              for (int j = 0; j < 2; ++j)       // 32-element halves of the block
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  dequant_word(w[2 * i + j], z2[2 * h + j], s2[2 * h + j], r + 16 * j + 4 * i);
-              if (h == 0) {
-                if (!wait(a_empty + 8 * ast, aph, DEVERR_TIMEOUT_EPI)) {
-                  ok = false;
-                  break;
-                }
-                tc_fence_after();
-              }
-              tmem_st32(trow + ast * W4_A_COLS + h * (W4_KB / 2), r);
-            }
-            if (!ok) break;
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive(a_full + 8 * ast);
+      for (int s = 0; s < nws; ++s) {
+        if (mine == 0) {
+          if (!wait(w_full + 8 * wst, wph, DEVERR_TIMEOUT_TMA)) {
+            ok = false;
+            break;
           }
-          if (++ast == AS) {
-            ast = 0;
-            aph ^= 1u;
+          const uint8_t* st = ws + wst * W4_W_STAGE;
+          const uint8_t* sc = st + W4_CODE_BYTES + side;
+          const uint8_t* zp = sc + W4_SIDE_BYTES;
+          // everything of the A stage's 128 k first: codes, scales, zero points (a block past K
+          // is read as zeros or the next matrix's scales, and no MMA takes it)
+          const uint8_t* src = st + row * 128;
+          uint4 c[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            c[i] = *reinterpret_cast<const uint4*>(src + (((2 * b0 + i) ^ (row & 7)) << 4));
+          __nv_bfloat162 s2[4], z2[4];        // per 32 k
+          const int at = ((W4_KB * b0) >> shift) * pitch;
+          s2[0] = scale_pair(sc[at]);
+          z2[0] = zero_pair(p.zeros ? zp[at] : 8u);
+          if (shift == 7) {
+            s2[1] = s2[2] = s2[3] = s2[0];
+            z2[1] = z2[2] = z2[3] = z2[0];
+          } else if (shift == 6) {
+            s2[1] = s2[0];
+            z2[1] = z2[0];
+            s2[2] = s2[3] = scale_pair(sc[at + pitch]);
+            z2[2] = z2[3] = zero_pair(p.zeros ? zp[at + pitch] : 8u);
+          } else {
+#pragma unroll
+            for (int i = 1; i < 4; ++i) {
+              s2[i] = scale_pair(sc[at + i * pitch]);
+              z2[i] = zero_pair(p.zeros ? zp[at + i * pitch] : 8u);
+            }
           }
+#pragma unroll
+          for (int h = 0; h < W4_KA / W4_KB; ++h) {
+            const uint4 lo = c[2 * h], hi = c[2 * h + 1];
+            const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            uint32_t r[32];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)       // 32-element halves of the block
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                dequant_word(w[2 * i + j], z2[2 * h + j], s2[2 * h + j], r + 16 * j + 4 * i);
+            if (h == 0) {
+              if (!wait(a_empty + 8 * set, aph, DEVERR_TIMEOUT_EPI)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+            }
+            tmem_st32(a_col + h * (W4_KB / 2), r);
+          }
+          if (!ok) break;
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            bar_arrive(a_full + 8 * set);
+            bar_arrive(w_empty + 8 * wst);
+          }
+          aph ^= 1u;
         }
-        __syncwarp();
-        if (lane == 0) bar_arrive(w_empty + 8 * wst);
+        if (DQ == 4) mine ^= 1u;
         if (++wst == WS) {
           wst = 0;
           wph ^= 1u;
@@ -593,7 +592,7 @@ template <int NT>
 size_t w4_smem(int G) {
   using S = W4Shape<NT>;
   return 1024 + (size_t)S::XS * NT * S::XK * 2 + (size_t)S::WS * W4_W_STAGE +
-         (2 * S::WS + 2 * S::XS + 2 * S::AS + 2 * S::ACCS + 1) * 8 + 8 +
+         (2 * S::WS + 2 * S::XS + 2 * S::DQ + 2 * S::ACCS + 1) * 8 + 8 +
          (size_t)2 * (G + 1) * sizeof(int);
 }
 
