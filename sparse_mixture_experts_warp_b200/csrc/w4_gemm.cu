@@ -127,13 +127,15 @@ __device__ __forceinline__ W4Tile w4_locate(int t, const int* grp_off, const int
   return r;
 }
 
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
-                                             uint32_t acc, uint32_t idesc) {
+// (the halves of the token descriptor apart: only the low one changes)
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                             uint32_t b_hi, uint32_t acc, uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc));
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc));
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
@@ -388,6 +390,8 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     uint32_t xph = 0, aph = 0;
     bool ok = true;
     const uint64_t bdesc = sdesc<W4_KB>(xs);
+    const uint32_t b_lo = (uint32_t)bdesc, b_hi = (uint32_t)(bdesc >> 32);
+    constexpr int HG = XB > 1 ? 2 : 1;          // 64-element blocks issued together
     for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++it) {
       const W4Tile tl = w4_locate<NT>(t, grp_off, tile_pre, g);
       const uint32_t idesc =
@@ -406,21 +410,27 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         }
         const uint32_t a0 = tmem_base + A_COL + ast * W4_A_COLS;
 #pragma unroll
-        for (int h = 0; h < W4_KA / W4_KB; ++h) {
-          if (kb + h >= nkb) break;
-          const int xb = (kb + h) % XB;         // box within the token stage
+        for (int h0 = 0; h0 < W4_KA / W4_KB; h0 += HG) {
+          if (kb + h0 >= nkb) break;
+          const int xb = (kb + h0) % XB;        // box within the token stage
           if (xb == 0 && !wait(x_full + 8 * xst, xph, DEVERR_TIMEOUT_MMA)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t b = bdesc + (uint32_t)((xst * X_STAGE + xb * X_BOX) >> 4);
-          const bool last = xb == XB - 1 || kb + h == nkb - 1;
+          const int end = min(HG, nkb - kb - h0);
+          const bool last = (kb + h0 + end) % XB == 0 || kb + h0 + end == nkb;
           if (leader) {
+            const uint32_t b = b_lo + (uint32_t)((xst * X_STAGE + xb * X_BOX) >> 4);
 #pragma unroll
-            for (int k = 0; k < W4_KB / 16; ++k)
-              umma_bf16_ts(d, a0 + h * (W4_KB / 2) + 8 * k, b + 2 * k, (kb | h | k) ? 1u : 0u,
-                           idesc);
+            for (int h = 0; h < HG; ++h) {
+              if (h && h >= end) break;
+#pragma unroll
+              for (int k = 0; k < W4_KB / 16; ++k)
+                umma_bf16_ts(d, a0 + (h0 + h) * (W4_KB / 2) + 8 * k,
+                             b + h * (X_BOX >> 4) + 2 * k, b_hi, (kb | h0 | h | k) ? 1u : 0u,
+                             idesc);
+            }
             if (last) bar_commit(x_empty + 8 * xst);
           }
           if (last && ++xst == XS) {
