@@ -79,7 +79,7 @@ template <> struct W4Shape<192> {
   static constexpr int WS = 3, XS = 6, XK = 64, XBOX = 64, ACCS = 2, DQ = 2, EPI = 2;
 };
 template <> struct W4Shape<128> {
-  static constexpr int WS = 6, XS = 3, XK = 128, XBOX = 64, ACCS = 2, DQ = 4, EPI = 1;
+  static constexpr int WS = 4, XS = 2, XK = 256, XBOX = 64, ACCS = 2, DQ = 4, EPI = 1;
 };
 template <> struct W4Shape<32> {
   static constexpr int WS = 8, XS = 4, XK = 256, XBOX = 32, ACCS = 2, DQ = 4, EPI = 1;
@@ -642,7 +642,9 @@ cudaError_t launch_w4_gemm(int act, const void* a, int64_t a_rows, int K, const 
   // 32 uneven groups of 2048 x 7168, 7 rows 187 / 194 / 215, 15 rows 214 / 195 / 216.
   const int64_t mean = (a_rows + G - 1) / G;
   const int nt_tok = mean > 96 ? 192 : mean > 12 ? 128 : 32;
-  const int xbox = nt_tok == 32 ? W4Shape<32>::XBOX : W4Shape<128>::XBOX;
+  const int xbox = nt_tok == 32    ? W4Shape<32>::XBOX
+                   : nt_tok == 128 ? W4Shape<128>::XBOX
+                                   : W4Shape<192>::XBOX;
   alignas(64) W4Maps m;
   auto maps = [&](const moe_w4_t* q, CUtensorMap* c, CUtensorMap* sc, CUtensorMap* z) {
     const int gs = W4_KS / q->group;
