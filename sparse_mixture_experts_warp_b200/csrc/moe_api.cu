@@ -758,15 +758,16 @@ static moe_status_t check_w4_up(const moe_desc_t* d, const moe_w4_t* gate, const
 
 // The streaming kernel reads a group's weights once per P rows (P: the tokens that fit its shared
 // memory, 8 up to K of about 6400, 3 at 14336), the tcgen05 kernel once per 32 to 192.  The first
-// is taken while the groups have about P rows on average.  Streaming / tcgen05, us, 8 groups of
-// 14336 x 4096, gate and up: 4 rows a group 131 / 197, 8 rows 178 / 197, 16 rows 306 / 199; down
-// (P = 3): 2 rows 69 / 109, 4 rows 97 / 109, 8 rows 162 / 109.  One group is cheap to pass over
-// twice (4096 x 4096, gate and up: 16 rows 17.6 / 19.5, 32 rows 24.9 / 20.2), hence G + 1.
+// is taken up to about two thirds of P rows a group.  Streaming / tcgen05, us, 8 groups of
+// 14336 x 4096, gate and up: 4 rows a group 131 / 161, 6 rows 149 / 161, 8 rows 178 / 161; down
+// (P = 3): 2 rows 69 / 92, 4 rows 98 / 89; 32 uneven groups of 2048 x 7168 (P = 7): 4 rows
+// 129 / 152, 7 rows 175 / 152; 64 uneven groups of 1408 x 2048: 3 rows 70 / 65, 6 rows 82 / 72;
+// one group of 4096 x 4096: 8 rows 13.0 / 16.6, 16 rows 17.7 / 16.6 (hence G + 1).
 static cudaError_t launch_w4_product(int act, const void* a, int64_t a_rows, int K,
                                      const moe_w4_t* gate, const moe_w4_t* w, int G, int N,
                                      const int32_t* offsets, void* out, cudaStream_t s) {
   const int64_t P = w4_stream_tokens(K, G);
-  const bool few = a_rows <= P * (G + 1);
+  const bool few = 3 * a_rows <= 2 * P * (G + 1);
   return few ? launch_w4_stream(act, a, a_rows, K, gate, w, G, N, offsets, out, s)
              : launch_w4_gemm(act, a, a_rows, K, gate, w, G, N, offsets, out, s);
 }

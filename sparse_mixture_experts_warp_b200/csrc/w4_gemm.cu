@@ -19,7 +19,7 @@
 //   warp 0       TMA producer of the weights: 256 k of codes (128 rows x 128 bytes, 128-byte
 //                swizzle: a thread's 16-byte reads of its row are free of bank conflicts), and
 //                their scales and zero points, per stage;
-//   warp 1       TMA producer of the token rows: 64 k (NT = 192) to 256 k (NT = 32) per stage, in
+//   warp 1       TMA producer of the token rows: 128 k (NT = 192) or 256 k per stage, in
 //                boxes of 64 k (128-byte swizzle) by the whole tile's rows, or by 64 of them where
 //                fewer do (up, Mixtral width, 2048 tokens: 989 us with boxes of 32 rows, 926 with
 //                64, 897 with 192);
@@ -27,24 +27,24 @@
 //   warp 3       group table;
 //   warps 4..    dequantisers: DQ sets of four warps, each takes every DQ-th
 //                128-element k-block, thread by thread 16 words -> 64 columns of packed bf16
-//                pairs (tcgen05.st), into the ring of A stages of 64 columns;
+//                pairs (tcgen05.st), into its A stage of 64 columns;
 //   then         epilogue: tcgen05.ld, row factor, activation, bf16 stores.
 // TMEM: two accumulators, so that the epilogue of a tile overlaps the next one's main loop, and a
-// ring of A stages: 2 x 192 and 2 x 64 columns, or 2 x 128 and 4 x 64.  (One accumulator of 256
+// A stage per dequantiser set: 2 x 192 and 2 x 64 columns, or 2 x 128 and 4 x 64.  (One accumulator of 256
 // columns left the tensor pipe idle for as long as an epilogue takes, a quarter of the time.)
 // When few tokens share a weight the loop has to run at the rate of the weights' bytes (a stage
 // of 16 KB of codes every 0.4 us), so stages are as long as memory allows: at 64-element A and
 // token stages the barrier traffic of the one MMA thread alone took 1.2 us for 16 KB.
 // What bounds it (8 groups of 14336 x 4096, gate and up): at 256 rows a group and more the pace of
-// the dequantisers and the MMAs together (2048 tokens: 816 to 847 us, 1.14 to 1.18 PFLOP/s under
-// the power cap, the tensor pipe 81% busy in the 703 us that one launch takes at full clock; before
-// the pairs' mask and magic became one step 818 us, of which 697 were left without the dequantising
-// arithmetic and 533 without the MMAs too).  At 8 to 64 rows a group about 200 us (2.4 TB/s of
-// codes): 164 to 194 without arithmetic and MMAs, so the hand-over from stage to stage.  Twice the
+// the dequantisers and the MMAs together, under the power cap (2048 tokens: about 800 us, 1.2
+// PFLOP/s; the tensor pipe was 81% busy in the 703 us that a launch of an earlier form took at full
+// clock).  At 8 to 64 rows a group 160 to 180 us (2.9 TB/s of codes): the MMA warp's own
+// instructions, which share a scheduler with four dequantisers, so what they cost counts: one
+// wait and branch for an A stage's eight MMAs and 32-bit descriptor arithmetic took 12 rows a group
+// from 183 to 157 us, token stages of 256 instead of 128 k 64 rows from 192 to 175.  Twice the
 // dequantisers (two warps a row, half an A stage each) made 2048 tokens 13% slower, a rolled loop
-// over an A stage's halves 15%, all eight MMAs of a stage behind one branch 27%, predicated MMAs
-// 7%; token boxes of exactly the tile's rows changed nothing at 12 rows a group and cost a third at
-// 512.
+// over an A stage's halves 15%, predicated MMAs 7%; token boxes of exactly the tile's rows changed
+// nothing at 12 rows a group and cost a third at 512.
 // Every mbarrier wait is bounded (globaltimer); a wait that gives up records an error code in
 // the device error word and the CTA drains what it has in flight and exits.
 #include <cuda.h>
@@ -76,7 +76,7 @@ constexpr int W4_FIRST_DQ = 4;
 // others could be two rounds ahead and take a wait's parity for their own.
 template <int NT> struct W4Shape;
 template <> struct W4Shape<192> {
-  static constexpr int WS = 3, XS = 6, XK = 64, XBOX = 64, ACCS = 2, DQ = 2, EPI = 2;
+  static constexpr int WS = 3, XS = 3, XK = 128, XBOX = 64, ACCS = 2, DQ = 2, EPI = 2;
 };
 template <> struct W4Shape<128> {
   static constexpr int WS = 4, XS = 2, XK = 256, XBOX = 64, ACCS = 2, DQ = 4, EPI = 1;
@@ -391,7 +391,7 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     bool ok = true;
     const uint64_t bdesc = sdesc<W4_KB>(xs);
     const uint32_t b_lo = (uint32_t)bdesc, b_hi = (uint32_t)(bdesc >> 32);
-    constexpr int HG = XB > 1 ? 2 : 1;          // 64-element blocks issued together
+    static_assert(XK % W4_KA == 0, "a token stage has whole A blocks");
     for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++it) {
       const W4Tile tl = w4_locate<NT>(t, grp_off, tile_pre, g);
       const uint32_t idesc =
@@ -409,27 +409,24 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
           break;
         }
         const uint32_t a0 = tmem_base + A_COL + ast * W4_A_COLS;
-#pragma unroll
-        for (int h0 = 0; h0 < W4_KA / W4_KB; h0 += HG) {
-          if (kb + h0 >= nkb) break;
-          const int xb = (kb + h0) % XB;        // box within the token stage
+        if (kb < nkb) {
+          const int xb = kb % XB;               // first of its boxes within the token stage
           if (xb == 0 && !wait(x_full + 8 * xst, xph, DEVERR_TIMEOUT_MMA)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const int end = min(HG, nkb - kb - h0);
-          const bool last = (kb + h0 + end) % XB == 0 || kb + h0 + end == nkb;
+          const int end = min(W4_KA / W4_KB, nkb - kb);
+          const bool last = (kb + end) % XB == 0 || kb + end == nkb;
           if (leader) {
             const uint32_t b = b_lo + (uint32_t)((xst * X_STAGE + xb * X_BOX) >> 4);
 #pragma unroll
-            for (int h = 0; h < HG; ++h) {
-              if (h && h >= end) break;
+            for (int h = 0; h < W4_KA / W4_KB; ++h) {
+              if (h >= end) break;
 #pragma unroll
               for (int k = 0; k < W4_KB / 16; ++k)
-                umma_bf16_ts(d, a0 + (h0 + h) * (W4_KB / 2) + 8 * k,
-                             b + h * (X_BOX >> 4) + 2 * k, b_hi, (kb | h0 | h | k) ? 1u : 0u,
-                             idesc);
+                umma_bf16_ts(d, a0 + h * (W4_KB / 2) + 8 * k, b + h * (X_BOX >> 4) + 2 * k, b_hi,
+                             (kb | h | k) ? 1u : 0u, idesc);
             }
             if (last) bar_commit(x_empty + 8 * xst);
           }
@@ -637,11 +634,11 @@ cudaError_t launch_w4_gemm(int act, const void* a, int64_t a_rows, int K, const 
   const bool glu = gate != nullptr;
   const int feats = glu ? 64 : 128;
   // Tokens per tile by the groups' mean rows; groups differ, so a tile holds more than the mean.
-  // Tiles of 32 / 128 / 192 tokens, us: 8 groups of 14336 x 4096, gate and up, 16 rows a group
-  // 199 / 205 / 227, 32 rows 271 / 208 / 230, 64 rows 453 / 210 / 265, 128 rows 830 / 332 / 277;
-  // 32 uneven groups of 2048 x 7168, 7 rows 187 / 194 / 215, 15 rows 214 / 195 / 216.
+  // Tiles of 32 / 128 / 192 tokens, us: 8 groups of 14336 x 4096, gate and up, 12 rows a group
+  // 161 / 163 / 181, 32 rows 216 / 174 / 199, 96 rows 523 / 204 / 259, 128 rows 674 / 298 / 264;
+  // 32 uneven groups of 2048 x 7168, 7 rows 152 / 161 / 175, 15 rows 174 / 164 / 177.
   const int64_t mean = (a_rows + G - 1) / G;
-  const int nt_tok = mean > 96 ? 192 : mean > 12 ? 128 : 32;
+  const int nt_tok = mean > 112 ? 192 : mean > 12 ? 128 : 32;
   const int xbox = nt_tok == 32    ? W4Shape<32>::XBOX
                    : nt_tok == 128 ? W4Shape<128>::XBOX
                                    : W4Shape<192>::XBOX;
