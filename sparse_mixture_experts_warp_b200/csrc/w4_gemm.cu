@@ -37,8 +37,7 @@
 // token stages the barrier traffic of the one MMA thread alone took 1.2 us for 16 KB.
 // What bounds it (8 groups of 14336 x 4096, gate and up): at 256 rows a group and more the pace of
 // the dequantisers and the MMAs together, under the power cap (2048 tokens: about 800 us, 1.2
-// PFLOP/s; the tensor pipe was 81% busy in the 703 us that a launch of an earlier form took at full
-// clock).  At 8 to 64 rows a group 160 to 180 us (2.9 TB/s of codes): the MMA warp's own
+// PFLOP/s; the tensor pipe is 81% busy in the 710 us that a single launch takes at full clock).  At 8 to 64 rows a group 160 to 180 us (2.9 TB/s of codes): the MMA warp's own
 // instructions, which share a scheduler with four dequantisers, so what they cost counts: one
 // wait and branch for an A stage's eight MMAs and 32-bit descriptor arithmetic took 12 rows a group
 // from 183 to 157 us, token stages of 256 instead of 128 k 64 rows from 192 to 175.  Twice the
