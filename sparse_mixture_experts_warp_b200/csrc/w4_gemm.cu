@@ -29,21 +29,23 @@
 //                128-element k-block, thread by thread 16 words -> 64 columns of packed bf16
 //                pairs (tcgen05.st), into its A stage of 64 columns;
 //   then         epilogue: tcgen05.ld, row factor, activation, bf16 stores.
-// TMEM: two accumulators, so that the epilogue of a tile overlaps the next one's main loop, and a
-// A stage per dequantiser set: 2 x 192 and 2 x 64 columns, or 2 x 128 and 4 x 64.  (One accumulator of 256
-// columns left the tensor pipe idle for as long as an epilogue takes, a quarter of the time.)
+// TMEM: two accumulators, so that the epilogue of a tile overlaps the next one's main loop, and
+// an A stage per dequantiser set: 2 x 192 and 2 x 64 columns, or 2 x 128 and 4 x 64.  (One
+// accumulator of 256 columns left the tensor pipe idle for as long as an epilogue takes, a
+// quarter of the time.)
 // When few tokens share a weight the loop has to run at the rate of the weights' bytes (a stage
 // of 16 KB of codes every 0.4 us), so stages are as long as memory allows: at 64-element A and
 // token stages the barrier traffic of the one MMA thread alone took 1.2 us for 16 KB.
-// What bounds it (8 groups of 14336 x 4096, gate and up): at 256 rows a group and more the pace of
-// the dequantisers and the MMAs together, under the power cap (2048 tokens: about 800 us, 1.2
-// PFLOP/s; the tensor pipe is 81% busy in the 710 us that a single launch takes at full clock).  At 8 to 64 rows a group 160 to 180 us (2.9 TB/s of codes): the MMA warp's own
-// instructions, which share a scheduler with four dequantisers, so what they cost counts: one
-// wait and branch for an A stage's eight MMAs and 32-bit descriptor arithmetic took 12 rows a group
-// from 183 to 157 us, token stages of 256 instead of 128 k 64 rows from 192 to 175.  Twice the
-// dequantisers (two warps a row, half an A stage each) made 2048 tokens 13% slower, a rolled loop
-// over an A stage's halves 15%, predicated MMAs 7%; token boxes of exactly the tile's rows changed
-// nothing at 12 rows a group and cost a third at 512.
+// What bounds it (8 groups of 14336 x 4096, gate and up): at 256 rows a group and more the pace
+// of the dequantisers and the MMAs together, under the power cap (2048 tokens: 780 to 850 us, 1.13
+// to 1.23 PFLOP/s; the tensor pipe is 81% busy in the 710 us that a single launch takes at full clock).
+// At 8 to 64 rows a group 160 to 180 us (2.9 TB/s of codes): the MMA warp's own instructions,
+// which share a scheduler with four dequantisers, so what they cost counts: one wait and branch
+// for an A stage's eight MMAs and 32-bit descriptor arithmetic took 12 rows a group from 183 to
+// 157 us, token stages of 256 instead of 128 k 64 rows from 192 to 175.  Twice the dequantisers
+// (two warps a row, half an A stage each) made 2048 tokens 13% slower, a rolled loop over an A
+// stage's halves 15%, predicated MMAs 7%; token boxes of exactly the tile's rows changed nothing
+// at 12 rows a group and cost a third at 512.
 // Every mbarrier wait is bounded (globaltimer); a wait that gives up records an error code in
 // the device error word and the CTA drains what it has in flight and exits.
 #include <cuda.h>
