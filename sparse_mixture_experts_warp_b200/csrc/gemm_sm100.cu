@@ -1265,18 +1265,35 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
+// Encodes a tensor map with dense elements; false when that fails.  The encoder is a driver call and
+// wants the device's context current on the calling thread, which a host thread's first runtime call
+// that needs it sees to: the address of the error word is one (it is allowed during a capture).
+bool encode_map(CUtensorMap* m, CUtensorMapDataType type, cuuint32_t rank, const void* ptr,
+                const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+                CUtensorMapSwizzle swizzle, CUtensorMapL2promotion l2) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint32_t estr[3] = {1, 1, 1};
+  auto run = [&] {
+    return enc(m, type, rank, const_cast<void*>(ptr), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, l2, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = run();
+  if (r == CUDA_ERROR_INVALID_CONTEXT || r == CUDA_ERROR_NOT_INITIALIZED) {
+    if (!device_error_word()) return false;
+    r = run();
+  }
+  return r == CUDA_SUCCESS;
+}
+
 // 3D fp32 tensor [groups][rows][cols] (dense); box = 16 columns x 32 rows x 1 group, 64-byte
 // swizzle (one 64-byte row of the box per swizzle row): the EPI_F32_TMA output.
 bool make_map_f32_out(CUtensorMap* m, void* ptr, uint64_t groups, uint64_t rows, uint64_t cols) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
   const cuuint64_t dims[3] = {cols, rows, groups};
   const cuuint64_t strides[2] = {cols * 4, rows * cols * 4};
   const cuuint32_t box[3] = {16, 32, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, ptr, dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
-             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, ptr, dims, strides, box,
+                    CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
 
@@ -1447,30 +1464,22 @@ cudaError_t launch_pair(int epi, const CUtensorMap& a, const CUtensorMap& b0,
 // 2-D bf16 tensor map (declared in tc_ops.cuh).
 bool make_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows,
               int kb) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
   const cuuint64_t dims[2] = {cols, rows};
   const cuuint64_t strides[1] = {cols * 2};
   const cuuint32_t box[2] = {(cuuint32_t)kb, box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box,
-             estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             kb == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ptr, dims, strides, box,
+                    kb == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 bool make_map_u8(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows,
                  uint32_t box_cols, bool swizzle) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
   const cuuint64_t dims[2] = {cols, rows};
   const cuuint64_t strides[1] = {cols};
   const cuuint32_t box[2] = {box_cols, box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE,
-             swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, ptr, dims, strides, box,
+                    swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 bool make_map_u8_3d(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t slices,
@@ -1481,10 +1490,8 @@ bool make_map_u8_3d(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t sli
   const cuuint64_t dims[3] = {pitch < 128 ? pitch : 128, rows, slices};
   const cuuint64_t strides[2] = {pitch, 128};
   const cuuint32_t box[3] = {128, box_rows, box_slices};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, ptr, dims, strides, box,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 bool gemm_gather_ok() {
