@@ -63,6 +63,16 @@ inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, siz
   return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
+constexpr size_t kMaxSmem = 227 * 1024;         // shared memory that a block can have
+
+// Lets `kern` have up to `bytes` of dynamic shared memory.  `bytes` is the same in every call for a
+// kernel, not what the launch at hand needs: the limit is the device's, so another host thread's
+// smaller launch would lower it between this call and the launch.
+template <typename K>
+inline cudaError_t allow_smem(K* kern, size_t bytes) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
 // ---- stream-K schedule of the fp32 k-split products (grouped GEMM and its summing kernel) ----
 // CTA c of g takes k-blocks [c * work / g, (c + 1) * work / g) of work = tiles * nkb (tile t
 // owns [t * nkb, (t + 1) * nkb)).  CTAs used: at most grid, and few enough that every range

@@ -99,6 +99,8 @@ template <> struct Eight<false> {
 // again for their codes.
 // Four words a lane: 8 took 295 us instead of 235 for 8 x 14336 x 4096 bf16, 2 took 348.
 constexpr int kMaxWarps = 16, kWords = 4;
+// the side tables of the longest rows (262144), groups of 32 with zero points, 4 rows a block
+constexpr size_t kQuantMaxSmem = 262144 / 32 * 2 * 4;
 
 template <bool BF16, bool ZEROS, int GROUP, bool TEAMS>
 __global__ void __launch_bounds__(32 * kMaxWarps)
@@ -355,8 +357,7 @@ cudaError_t launch_quantize_w4(int n_matrices, int N, int K, bool bf16, const vo
   while (per == 4 && teams < 4 && 2 * teams * warps <= kMaxWarps) teams *= 2;
   auto go = [&](auto k) {
     if (smem > 40960) {
-      cudaError_t e =
-          cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      cudaError_t e = allow_smem(k, kQuantMaxSmem);
       if (e != cudaSuccess) return e;
     }
     return launch_pdl(k, dim3((unsigned)(rows / per)), dim3(32 * warps * teams), smem, s, W, N, K,

@@ -597,7 +597,7 @@ w4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
 }
 
 template <int NT>
-size_t w4_smem(int G) {
+constexpr size_t w4_smem(int G) {
   using S = W4Shape<NT>;
   return 1024 + (size_t)S::XS * NT * S::XK * 2 + (size_t)S::WS * W4_W_STAGE +
          (2 * S::WS + 2 * S::XS + 2 * S::DQ + 2 * S::ACCS + 1) * 8 + 8 +
@@ -612,12 +612,13 @@ template <int NT, bool GLU>
 cudaError_t launch(const W4Maps& m, const W4Params& p, int64_t a_rows, cudaStream_t s) {
   const size_t smem = w4_smem<NT>(p.G);
   auto kern = w4_gemm_kernel<NT, GLU>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  constexpr size_t most = w4_smem<NT>(1024);    // (groups of a call)
+  static_assert(most <= kMaxSmem, "shared memory");
+  cudaError_t e = allow_smem(kern, most);
   if (e != cudaSuccess) return e;
-  const int64_t most = ((a_rows + NT - 1) / NT + p.G) * (int64_t)p.nt;
+  const int64_t tiles = ((a_rows + NT - 1) / NT + p.G) * (int64_t)p.nt;
   const int sms = gemm_sm_count();
-  const int grid = (int)(most < sms ? most : sms);
+  const int grid = (int)(tiles < sms ? tiles : sms);
   return launch_pdl(kern, dim3(grid), dim3(w4_threads<NT>()), smem, s, m.x, m.xall, m.c0, m.c1,
                     m.s0, m.s1, m.z0, m.z1, p);
 }

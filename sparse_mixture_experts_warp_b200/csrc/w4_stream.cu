@@ -49,7 +49,6 @@ constexpr int ST_PART = 16 * ST_TOK;            // fp32 partial sums of a warp
 constexpr int ST_XPAD = 64;                     // bytes: rows of x start 64 bytes apart mod 128
 constexpr size_t ST_FIXED = 1024 + (size_t)ST_STAGES * ST_STAGE + 2 * ST_WARPS * ST_PART * 4 +
                             2 * ST_STAGES * 8 + 16 + 4 * ST_TOK * 4;
-constexpr size_t ST_SMEM = 227 * 1024;
 
 struct StreamParams {
   const __nv_bfloat16* a;                       // [rows, K]
@@ -451,8 +450,8 @@ w4_stream_kernel(const __grid_constant__ StreamMaps m0, const __grid_constant__ 
 // Tokens per tile that the shared memory holds next to the rings; 0: K is too long.
 int w4_stream_tokens(int K, int G) {
   const size_t table = (size_t)2 * (G + 1) * sizeof(int);
-  if (ST_FIXED + table >= ST_SMEM) return 0;
-  const size_t n = (ST_SMEM - ST_FIXED - table) / (2 * (size_t)K + ST_XPAD);
+  if (ST_FIXED + table >= kMaxSmem) return 0;
+  const size_t n = (kMaxSmem - ST_FIXED - table) / (2 * (size_t)K + ST_XPAD);
   return n < ST_TOK ? (int)n : ST_TOK;
 }
 
@@ -507,8 +506,7 @@ cudaError_t launch_w4_stream(int act, const void* a, int64_t a_rows, int K, cons
   const size_t smem = ST_FIXED + (size_t)p.P * (2 * (size_t)K + ST_XPAD) +
                       (size_t)2 * (G + 1) * sizeof(int);
   auto run = [&](auto kern) {
-    cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(kern, kMaxSmem);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(grid), dim3(ST_THREADS), smem, s, m0, m1, p);
   };
