@@ -72,7 +72,7 @@ cudaError_t launch_ffn_up_f32(int act, const float* a, int64_t a_rows, int D, in
   if (a_rows <= 0) return cudaSuccess;
   const size_t smem = (size_t)D * sizeof(float);
   if (smem > 48 * 1024)
-    cudaFuncSetAttribute(ffn_up_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    (void)allow_smem(ffn_up_f32_kernel, kMaxSmem);
   ffn_up_f32_kernel<<<counted((unsigned)a_rows), 128, smem, s>>>(a, D, F, offsets, n_groups, Wgate, Wup,
                                                         act, h);
   return cudaGetLastError();
@@ -84,7 +84,7 @@ cudaError_t launch_ffn_down_f32(const float* h, int64_t a_rows, int D, int F,
   if (a_rows <= 0) return cudaSuccess;
   const size_t smem = (size_t)F * sizeof(float);
   if (smem > 48 * 1024)
-    cudaFuncSetAttribute(ffn_down_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    (void)allow_smem(ffn_down_f32_kernel, kMaxSmem);
   ffn_down_f32_kernel<<<counted((unsigned)a_rows), 128, smem, s>>>(h, D, F, offsets, n_groups, Wdown, y);
   return cudaGetLastError();
 }

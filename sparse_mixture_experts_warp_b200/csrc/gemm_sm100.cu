@@ -1372,8 +1372,7 @@ template <int EPI, int HALVES, int KB, int NSTAGES, int RB = BM>
 cudaError_t launch_epi(const CUtensorMap& a, const CUtensorMap& b0, const CUtensorMap& b1,
                        const GemmParams& p, int grid, size_t smem, cudaStream_t s) {
   auto kern = grouped_gemm_kernel<EPI, HALVES, KB, NSTAGES, RB>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+  cudaError_t e = allow_smem(kern, kMaxSmem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(grid), dim3(64 + 128 * HALVES), smem, s, a, b0, b1, p);
 }
@@ -1439,8 +1438,7 @@ cudaError_t launch_pair_epi(const CUtensorMap& a, const CUtensorMap& b0, const C
                             const GemmParams& p, int64_t max_tiles, cudaStream_t s) {
   auto kern = grouped_gemm_pair_kernel<EPI, kPairStages>;
   const size_t smem = pair_smem(kPairStages, p.G);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+  cudaError_t e = allow_smem(kern, kMaxSmem);
   if (e != cudaSuccess) return e;
   const int slots = pair_slots<EPI>(smem);
   const int pairs = (int)(max_tiles < slots ? max_tiles : slots);
@@ -1575,7 +1573,6 @@ cudaError_t launch_grouped_gemm_bf16(int epi, const void* A, int64_t a_rows, int
     return launch_pair(epi, ta, tb0, tb1, p, pair_tiles, s);
   }
   const int grid = (int)(max_tiles < sm_count() ? max_tiles : sm_count());
-  constexpr size_t kMaxSmem = 232448;          // 227 KB of dynamic shared memory per block
   switch (tile) {
     case TILE_128:
       return launch_cfg<1, 64, 4>(epi, ta, tb0, tb1, p, grid, gemm_smem(1, 64, 4, n_groups), s);
@@ -1650,7 +1647,6 @@ cudaError_t launch_grouped_gemm_kgroups_f32(const void* A, int M, const void* B,
   if (M <= 0 || N <= 0 || G <= 0) return cudaSuccess;
   // The output needs 16-byte aligned rows: N a multiple of 4.
   if (N % 4 || (reinterpret_cast<uintptr_t>(out) & 15)) return cudaErrorInvalidValue;
-  constexpr size_t kMaxSmem = 232448;          // 227 KB of dynamic shared memory per block
   const bool t128 = wgrad_tile_128();
   const int halves = t128 ? 1 : 2;
   const size_t staging = (size_t)4 * halves * 2 * 2048;   // two 2 KB buffers per epilogue warp

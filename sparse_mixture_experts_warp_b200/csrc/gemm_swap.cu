@@ -406,8 +406,7 @@ template <int EPI, bool GATHER>
 cudaError_t launch_swap_epi(const CUtensorMap& x, const CUtensorMap& w0, const CUtensorMap& w1,
                             const SwapParams& p, int grid, size_t smem, cudaStream_t s) {
   auto kern = grouped_gemm_swap_kernel<EPI, GATHER>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+  cudaError_t e = allow_smem(kern, kMaxSmem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(grid), dim3(SW_THREADS), smem, s, x, w0, w1, p);
 }

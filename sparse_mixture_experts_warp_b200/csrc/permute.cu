@@ -654,8 +654,8 @@ cudaError_t launch_permute_token_choice(const moe_desc_t& d, const int32_t* ids,
     const int chunk = ((A + ncta - 1) / ncta + 1023) / 1024 * 1024;
     ncta = (A + chunk - 1) / chunk;
     const size_t smem = ((size_t)35 * E + chunk) * sizeof(int);
-    cudaError_t e = cudaFuncSetAttribute(perm_index_cluster_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    constexpr size_t most = (35 * 1024 + kClusterMaxItems / kClusterMaxCTAs) * sizeof(int);
+    cudaError_t e = allow_smem(perm_index_cluster_kernel, most);
     if (e != cudaSuccess) return e;
     note_launch();
     cudaLaunchConfig_t cfg = {};
@@ -678,8 +678,7 @@ cudaError_t launch_permute_token_choice(const moe_desc_t& d, const int32_t* ids,
   } else if (A <= kFusedMaxItems) {
     const size_t smem = ((size_t)33 * E + A) * sizeof(int);
     if (smem > 48 * 1024)
-      cudaFuncSetAttribute(perm_index_fused_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)smem);
+      (void)allow_smem(perm_index_fused_kernel, kMaxSmem - 1024);     // (less its static part)
     (void)launch_pdl(perm_index_fused_kernel, dim3(1), dim3(1024), smem, s, ids, A, E, cap, counts, offsets, row_src, inv);
   } else {
     (void)launch_pdl(perm_hist_kernel, dim3(nblk), dim3(kThreads), E * sizeof(int), s, ids, A, E, block_hist);

@@ -569,8 +569,7 @@ static void launch_router_tpw(const RouterArgs& a, int T, cudaStream_t s) {
   if (words < part_words) words = part_words;
   const size_t smem = words * sizeof(float);
   if (smem > 48 * 1024)
-    cudaFuncSetAttribute(router_kernel<BF16, TPW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         (int)smem);
+    (void)allow_smem(router_kernel<BF16, TPW>, kMaxSmem - 1024);      // (less its static part)
   (void)launch_pdl(router_kernel<BF16, TPW>, dim3(blocks), dim3(kWarps * 32), smem, s, a);
 }
 
@@ -680,10 +679,10 @@ cudaError_t launch_router_expert_choice(const moe_desc_t& d, const void* x, cons
 cudaError_t launch_ec_select(const moe_desc_t& d, const float* probsT, int32_t* picked,
                              cudaStream_t s) {
   const size_t smem = (size_t)d.T * sizeof(float);
-  if (d.T % 4 == 0 && smem <= 180 * 1024) {      // + 33 KB of static shared memory
+  constexpr size_t kEcMaxSmem = 180 * 1024;      // + 33 KB of static shared memory
+  if (d.T % 4 == 0 && smem <= kEcMaxSmem) {
     if (smem > 48 * 1024) {
-      cudaError_t e = cudaFuncSetAttribute(ec_select_kernel<true>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      cudaError_t e = allow_smem(ec_select_kernel<true>, kEcMaxSmem);
       if (e != cudaSuccess) return e;
     }
     (void)launch_pdl(ec_select_kernel<true>, dim3(d.E), dim3(1024), smem, s, probsT, d.T, d.c, picked);

@@ -350,7 +350,7 @@ cudaError_t launch_router_tc(const moe_desc_t& d, const RouterArgs& a, int* n_pa
   const RtConfig c = rt_config(d);
   *n_partials = c.grid;
   if (c.grid == 0) return cudaSuccess;
-  if (c.smem > 227 * 1024) return cudaErrorInvalidValue;
+  if (c.smem > kMaxSmem) return cudaErrorInvalidValue;
   alignas(64) CUtensorMap tx, tw;
   if (!make_map(&tx, a.x, (uint64_t)d.T, (uint64_t)d.D, kRtRows, kRtKB)) return cudaErrorInvalidValue;
   if (!make_map(&tw, a.Wg, (uint64_t)d.E, (uint64_t)d.D, (uint32_t)c.npad, kRtKB))
@@ -368,8 +368,7 @@ cudaError_t launch_router_tc(const moe_desc_t& d, const RouterArgs& a, int* n_pa
   void (*kern)(CUtensorMap, CUtensorMap, RtParams) =
       d.E <= 32 ? router_tc_kernel<1> : d.E <= 64 ? router_tc_kernel<2>
                                       : d.E <= 128 ? router_tc_kernel<4> : router_tc_kernel<8>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)c.smem);
+  cudaError_t e = allow_smem(kern, kMaxSmem);
   if (e != cudaSuccess) return e;
   note_launch();
   cudaLaunchConfig_t cfg = {};
