@@ -428,13 +428,15 @@ w4_stream_kernel(const __grid_constant__ StreamMaps m0, const __grid_constant__ 
           v += src[w * ST_PART + tok];
           if (GLU) u += src[w * ST_PART + 8 * ST_TOK + tok];
         }
+        // one after the other: a small row's power times a small row factor can be 0 or subnormal
+        // where the result is not
         const float bk = back[xbuf * ST_TOK + tok];
         if (GLU) {
-          v *= bk * rs_gate;
-          u *= bk * rs_w;
+          v = v * bk * rs_gate;
+          u = u * bk * rs_w;
           v = __fdividef(v, 1.0f + __expf(-v)) * u;
         } else {
-          v *= bk * rs_w;
+          v = v * bk * rs_w;
           if (p.act == MOE_ACT_RELU) v = v < 0.f ? 0.f : v;          // a NaN stays one
           if (p.act == MOE_ACT_GELU) v = 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
         }
