@@ -498,6 +498,12 @@ class W4:
     def __setattr__(self, name, value):
         raise AttributeError(f"the {name} of 4-bit weights is fixed; make another W4")
 
+    def __reduce__(self):
+        """Copies and pickles are made from the tensors, since the C struct holds addresses (the
+        scales as bytes: pickle knows no storage of 8-bit floats)."""
+        return _w4_of_bytes, (self.codes, self.scales.view(torch.uint8), self.zeros,
+                              self.row_scale, self.group)
+
     def _ref(self):
         """The C struct, with the addresses that the tensors have now."""
         c = self._c
@@ -505,6 +511,10 @@ class W4:
         c.zeros = self.zeros.data_ptr() if self.zeros is not None else None
         c.row_scale = self.row_scale.data_ptr()
         return ctypes.byref(c)
+
+
+def _w4_of_bytes(codes, scales, zeros, row_scale, group) -> W4:
+    return W4(codes, scales.view(torch.float8_e4m3fn), zeros, row_scale, group)
 
 
 def empty_w4(G, N, K, group=128, zeros=False, device="cuda") -> W4:
