@@ -414,7 +414,8 @@ moe_status_t moe_layer_forward_train(const moe_desc_t* desc, const void* x, cons
  *   gradient that reaches x by other ways (router, shared experts, residual).  dx may be add
  *   itself.
  * Sums are fp32 in a fixed order (no atomics), rounded once; inv must name rows below A, each at
- * most once, as moe_permute leaves it.  T = 0 returns MOE_OK without a launch. */
+ * most once, as moe_permute leaves it.  T = 0 returns MOE_OK without a launch, whatever the
+ * buffers (a tensor without elements may have no address). */
 moe_status_t moe_combine_backward(const moe_desc_t* desc, const void* dout, const void* y,
                                   const int32_t* inv, const float* gates, void* dy,
                                   float* dgates, moe_stream_t stream);
@@ -454,7 +455,7 @@ typedef struct moe_w4 {
  *   code = clamp(rint(w * (1 / step)) + zero, 0, 15).
  * A row of zeros (largest t below 2^-100) has row_scale 0; a row that holds a NaN or an infinity
  * stands for NaN.  moe_dequantize_w4 writes the values W stands for, rounded once to dtype.
- * 0 <= n_matrices; n_matrices * N < 2^31; K <= 262144. */
+ * 0 <= n_matrices (with 0 the arrays may be NULL); n_matrices * N < 2^31; K <= 262144. */
 moe_status_t moe_quantize_w4(int32_t n_matrices, int32_t N, int32_t K, int32_t dtype,
                              const void* W, const moe_w4_t* out, moe_stream_t stream);
 moe_status_t moe_dequantize_w4(int32_t n_matrices, int32_t N, int32_t K, const moe_w4_t* w,
@@ -465,7 +466,8 @@ moe_status_t moe_dequantize_w4(int32_t n_matrices, int32_t N, int32_t K, const m
  * [n_groups, D, F].  a, h, y bf16 (MOE_ERR_UNSUPPORTED for fp32 layers), fp32 sums; the other
  * arguments and the rows written are those of moe_expert_up / moe_expert_down, and results are
  * those of the values the weights stand for, but that a row's elements may enter with an error of
- * up to 2^-39 of its largest one.  No scratch. */
+ * up to 2^-39 of its largest one.  a_rows = 0 returns MOE_OK without a launch; a and h / y may then
+ * be NULL.  No scratch. */
 moe_status_t moe_expert_up_w4(const moe_desc_t* desc, int32_t n_groups, int32_t F,
                               const void* a, int64_t a_rows, const int32_t* offsets,
                               const moe_w4_t* gate, const moe_w4_t* up, void* h,
@@ -475,7 +477,7 @@ moe_status_t moe_expert_down_w4(const moe_desc_t* desc, int32_t n_groups, int32_
                                 const moe_w4_t* down, void* y, moe_stream_t stream);
 
 /* moe_layer_forward with the routed experts' weights in 4 bits; the router and the shared experts
- * keep bf16 weights.  Same steps, workspace, views and statistics. */
+ * keep bf16 weights.  Same steps, workspace, views and statistics; with T = 0 x and out may be NULL. */
 moe_status_t moe_layer_forward_w4(const moe_desc_t* desc, const void* x, const void* Wg,
                                   const float* sel_bias, const moe_w4_t* gate,
                                   const moe_w4_t* up, const moe_w4_t* down, const void* Ws_gate,

@@ -500,7 +500,7 @@ class W4:
 
     def __reduce__(self):
         """Copies and pickles are made from the tensors, since the C struct holds addresses (the
-        scales as bytes: pickle knows no storage of 8-bit floats)."""
+        scales as bytes: torch does not read a pickled tensor of 8-bit floats back)."""
         return _w4_of_bytes, (self.codes, self.scales.view(torch.uint8), self.zeros,
                               self.row_scale, self.group)
 

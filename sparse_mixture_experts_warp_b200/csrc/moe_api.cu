@@ -416,11 +416,13 @@ moe_status_t moe_permute(const moe_desc_t* d, const int32_t* expert_ids, const v
   return cuda_status(e);
 }
 
+// empty_ok: without rows, `a` may be a tensor without an address
 static moe_status_t check_ffn(const moe_desc_t* d, int32_t G, int32_t F, const void* a,
-                              int64_t a_rows, const int32_t* offsets) {
+                              int64_t a_rows, const int32_t* offsets, bool empty_ok = false) {
   moe_status_t st = validate(d);
   if (st != MOE_OK) return st;
-  if (G < 1 || G > 1024 || F <= 0 || a_rows < 0 || !a || !offsets) return MOE_ERR_INVALID_ARG;
+  if (G < 1 || G > 1024 || F <= 0 || a_rows < 0 || !offsets) return MOE_ERR_INVALID_ARG;
+  if (!a && !(empty_ok && a_rows == 0)) return MOE_ERR_INVALID_ARG;
   if (!is_aligned16(a)) return MOE_ERR_INVALID_ARG;
   if (d->dtype == MOE_BF16 && (F % 64)) return MOE_ERR_UNSUPPORTED;
   if (a_rows >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
@@ -688,6 +690,7 @@ moe_status_t moe_combine_backward(const moe_desc_t* d, const void* dout, const v
                                   float* dgates, moe_stream_t stream) {
   moe_status_t st = validate(d);
   if (st != MOE_OK) return st;
+  if (d->T == 0) return MOE_OK;                 // (tensors without elements have no address)
   if (!dout || !inv || !gates || (!dy && !dgates) || (dgates && !y)) return MOE_ERR_INVALID_ARG;
   if (!is_aligned16(dout) || !is_aligned16(y) || !is_aligned16(inv) || !is_aligned16(gates) ||
       !is_aligned16(dy) || !is_aligned16(dgates))
@@ -700,6 +703,7 @@ moe_status_t moe_permute_backward(const moe_desc_t* d, const void* dx_perm, cons
                                   const void* add, void* dx, moe_stream_t stream) {
   moe_status_t st = validate(d);
   if (st != MOE_OK) return st;
+  if (d->T == 0) return MOE_OK;
   if (!dx_perm || !inv || !dx) return MOE_ERR_INVALID_ARG;
   if (!is_aligned16(dx_perm) || !is_aligned16(inv) || !is_aligned16(add) || !is_aligned16(dx))
     return MOE_ERR_INVALID_ARG;
@@ -709,8 +713,9 @@ moe_status_t moe_permute_backward(const moe_desc_t* d, const void* dx_perm, cons
 
 // ---- 4-bit expert weights ----
 
-static moe_status_t check_w4(const moe_w4_t* w) {
-  if (!w || !w->codes || !w->scales || !w->row_scale) return MOE_ERR_INVALID_ARG;
+// empty: weights of no matrices, whose arrays have no address
+static moe_status_t check_w4(const moe_w4_t* w, bool empty = false) {
+  if (!w || (!empty && (!w->codes || !w->scales || !w->row_scale))) return MOE_ERR_INVALID_ARG;
   if (!is_aligned16(w->codes) || !is_aligned16(w->scales) || !is_aligned16(w->zeros) ||
       !is_aligned16(w->row_scale))
     return MOE_ERR_INVALID_ARG;
@@ -721,9 +726,9 @@ static moe_status_t check_w4(const moe_w4_t* w) {
 
 static moe_status_t check_w4_convert(int32_t n, int32_t N, int32_t K, int32_t dtype,
                                      const void* W, const moe_w4_t* w) {
-  if (n < 0 || N <= 0 || K <= 0 || !W || !is_aligned16(W)) return MOE_ERR_INVALID_ARG;
+  if (n < 0 || N <= 0 || K <= 0 || (n > 0 && !W) || !is_aligned16(W)) return MOE_ERR_INVALID_ARG;
   if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
-  const moe_status_t st = check_w4(w);
+  const moe_status_t st = check_w4(w, n == 0);
   if (st != MOE_OK) return st;
   if (N % 64 || K % 64 || K > 262144 || (int64_t)n * N >= ((int64_t)1 << 31))
     return MOE_ERR_UNSUPPORTED;
@@ -775,11 +780,11 @@ static cudaError_t launch_w4_product(int act, const void* a, int64_t a_rows, int
 moe_status_t moe_expert_up_w4(const moe_desc_t* d, int32_t G, int32_t F, const void* a,
                               int64_t a_rows, const int32_t* offsets, const moe_w4_t* gate,
                               const moe_w4_t* up, void* h, moe_stream_t stream) {
-  moe_status_t st = check_ffn(d, G, F, a, a_rows, offsets);
+  moe_status_t st = check_ffn(d, G, F, a, a_rows, offsets, true);
   if (st != MOE_OK) return st;
   st = check_w4_up(d, gate, up);
   if (st != MOE_OK) return st;
-  if (!h || !is_aligned16(h)) return MOE_ERR_INVALID_ARG;
+  if ((a_rows > 0 && !h) || !is_aligned16(h)) return MOE_ERR_INVALID_ARG;
   const bool glu = d->act == MOE_ACT_SWIGLU;
   return cuda_status(launch_w4_product(d->act, a, a_rows, d->D, glu ? gate : nullptr, up, G, F,
                                        offsets, h, reinterpret_cast<cudaStream_t>(stream)));
@@ -788,12 +793,12 @@ moe_status_t moe_expert_up_w4(const moe_desc_t* d, int32_t G, int32_t F, const v
 moe_status_t moe_expert_down_w4(const moe_desc_t* d, int32_t G, int32_t F, const void* h,
                                 int64_t a_rows, const int32_t* offsets, const moe_w4_t* down,
                                 void* y, moe_stream_t stream) {
-  moe_status_t st = check_ffn(d, G, F, h, a_rows, offsets);
+  moe_status_t st = check_ffn(d, G, F, h, a_rows, offsets, true);
   if (st != MOE_OK) return st;
   if (d->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   st = check_w4(down);
   if (st != MOE_OK) return st;
-  if (!y || !is_aligned16(y)) return MOE_ERR_INVALID_ARG;
+  if ((a_rows > 0 && !y) || !is_aligned16(y)) return MOE_ERR_INVALID_ARG;
   return cuda_status(launch_w4_product(-1, h, a_rows, F, nullptr, down, G, d->D, offsets, y,
                                        reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -845,7 +850,9 @@ static moe_status_t forward_impl(const moe_desc_t* d, const void* x, const void*
   moe_layer_views_t v;
   moe_status_t st = moe_layer_views(d, ws, ws_bytes, &v);
   if (st != MOE_OK) return st;
-  if (!x || !Wg || !out || (!w4 && (!W_up || !W_down))) return MOE_ERR_INVALID_ARG;
+  // (a 4-bit layer without tokens takes x and out without an address)
+  if (!Wg || (!w4 && (!W_up || !W_down))) return MOE_ERR_INVALID_ARG;
+  if ((!x || !out) && !(w4 && d->T == 0)) return MOE_ERR_INVALID_ARG;
   if (!w4 && d->act == MOE_ACT_SWIGLU && !W_gate) return MOE_ERR_INVALID_ARG;
   if (d->n_shared > 0 && (!Ws_gate || !Ws_up || !Ws_down)) return MOE_ERR_INVALID_ARG;
   if (d->T == 0) return MOE_OK;

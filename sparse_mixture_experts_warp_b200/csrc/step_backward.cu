@@ -193,7 +193,6 @@ int vectors_of(const moe_desc_t& d) { return d.D / (d.dtype == MOE_BF16 ? 8 : 4)
 cudaError_t launch_combine_backward(const moe_desc_t& d, const void* dout, const void* y,
                                     const int32_t* inv, const float* gates, void* dy,
                                     float* dgates, cudaStream_t s) {
-  if (d.T == 0) return cudaSuccess;
   const int nvec = vectors_of(d);
   int W = 1;
   while (W < kWarps && W * kSpan < nvec) W *= 2;
@@ -208,7 +207,6 @@ cudaError_t launch_combine_backward(const moe_desc_t& d, const void* dout, const
 cudaError_t launch_permute_backward(const moe_desc_t& d, const void* dx_perm,
                                     const int32_t* inv, const void* add, void* dx,
                                     cudaStream_t s) {
-  if (d.T == 0) return cudaSuccess;
   const int nvec = vectors_of(d);
   const int spans = (nvec + kSpan - 1) / kSpan;
   const int64_t warps = (int64_t)d.T * spans;
