@@ -399,7 +399,9 @@ moe_status_t moe_layer_forward_train(const moe_desc_t* desc, const void* x, cons
 
 /* Gradients of the dispatch and of the merge, for layers whose experts are the caller's own: with
  * moe_route, moe_permute and moe_combine they are the steps around any expert network (Tiny MoE
- * sections 5, 6 and 9; "Top-k 路由" section "門控網路的梯度流").  The selection is fixed.
+ * sections 5, 6 and 9; "Top-k 路由" section "門控網路的梯度流").  The selection is fixed; the way on
+ * from dgates through the gates' scores to Wg and x is the caller's (moe_layer_backward has it for
+ * the built-in experts).
  *
  * moe_combine_backward: out[t] = sum_j gates[t,j] * y[inv[t,j]] gives
  *     dy[inv[t,j]] = gates[t,j] * dout[t],   dgates[t,j] = <dout[t], y[inv[t,j]]>,
@@ -453,8 +455,9 @@ typedef struct moe_w4 {
  *   code = clamp(rint(w * (1 / step)), -8, 7) + 8, with zero points
  *   zero = clamp(rint(-min(w, 0) * (1 / step)), 0, 15) and
  *   code = clamp(rint(w * (1 / step)) + zero, 0, 15).
- * A row of zeros (largest t below 2^-100) has row_scale 0; a row that holds a NaN or an infinity
- * stands for NaN.  moe_dequantize_w4 writes the values W stands for, rounded once to dtype.
+ * A row of zeros (largest t below 2^-100) has row_scale 0; a row that holds a NaN or an infinity,
+ * or with zero points a group whose max - min overflows, stands for NaN.  moe_dequantize_w4 writes
+ * row_scale * (scale * (code - zero)) as one fp32 product, for MOE_BF16 rounded from there.
  * 0 <= n_matrices (with 0 the arrays may be NULL); n_matrices * N < 2^31; K <= 262144. */
 moe_status_t moe_quantize_w4(int32_t n_matrices, int32_t N, int32_t K, int32_t dtype,
                              const void* W, const moe_w4_t* out, moe_stream_t stream);
@@ -466,8 +469,10 @@ moe_status_t moe_dequantize_w4(int32_t n_matrices, int32_t N, int32_t K, const m
  * [n_groups, D, F].  a, h, y bf16 (MOE_ERR_UNSUPPORTED for fp32 layers), fp32 sums; the other
  * arguments and the rows written are those of moe_expert_up / moe_expert_down, and results are
  * those of the values the weights stand for, but that a row's elements may enter with an error of
- * up to 2^-39 of its largest one.  a_rows = 0 returns MOE_OK without a launch; a and h / y may then
- * be NULL.  No scratch. */
+ * up to 2^-39 of its largest one.  a_rows, rows behind the last group included, chooses the kernel
+ * (few rows a group stream the weights, more run on tcgen05), so a buffer far taller than its groups
+ * need costs time.  a_rows = 0 returns MOE_OK without a launch; a and h / y may then be NULL.  No
+ * scratch. */
 moe_status_t moe_expert_up_w4(const moe_desc_t* desc, int32_t n_groups, int32_t F,
                               const void* a, int64_t a_rows, const int32_t* offsets,
                               const moe_w4_t* gate, const moe_w4_t* up, void* h,
@@ -477,7 +482,8 @@ moe_status_t moe_expert_down_w4(const moe_desc_t* desc, int32_t n_groups, int32_
                                 const moe_w4_t* down, void* y, moe_stream_t stream);
 
 /* moe_layer_forward with the routed experts' weights in 4 bits; the router and the shared experts
- * keep bf16 weights.  Same steps, workspace, views and statistics; with T = 0 x and out may be NULL. */
+ * keep bf16 weights.  Same steps, workspace, views and statistics; with T = 0 x and out may be
+ * NULL. */
 moe_status_t moe_layer_forward_w4(const moe_desc_t* desc, const void* x, const void* Wg,
                                   const float* sel_bias, const moe_w4_t* gate,
                                   const moe_w4_t* up, const moe_w4_t* down, const void* Ws_gate,

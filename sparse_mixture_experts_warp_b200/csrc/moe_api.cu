@@ -763,11 +763,16 @@ static moe_status_t check_w4_up(const moe_desc_t* d, const moe_w4_t* gate, const
 
 // The streaming kernel reads a group's weights once per P rows (P: the tokens that fit its shared
 // memory, 8 up to K of about 6400, 3 at 14336), the tcgen05 kernel once per 32 to 192.  The first
-// is taken up to about two thirds of P rows a group.  Streaming / tcgen05, us, 8 groups of
-// 14336 x 4096, gate and up: 4 rows a group 131 / 161, 6 rows 149 / 161, 8 rows 178 / 161; down
-// (P = 3): 2 rows 69 / 92, 4 rows 98 / 89; 32 uneven groups of 2048 x 7168 (P = 7): 4 rows
-// 129 / 152, 7 rows 175 / 152; 64 uneven groups of 1408 x 2048: 3 rows 70 / 65, 6 rows 82 / 72;
-// one group of 4096 x 4096: 8 rows 13.0 / 16.6, 16 rows 17.7 / 16.6 (hence G + 1).
+// is taken up to about two thirds of P rows a group, counted as a_rows / G: how the rows lie, and
+// how many are behind the last group, only the device knows.  Streaming / tcgen05, us, mean rows of
+// routed groups: 8 of 14336 x 4096, gate and up, 4 rows 131 / 161, 6 rows 149 / 161, 8 rows
+// 178 / 161; down (P = 3), 2 rows 69 / 92, 4 rows 97 / 89; 32 of 2048 x 7168 (P = 7), 4 rows
+// 129 / 152, 7 rows 175 / 152; 64 of 1408 x 2048 with zero points, 3 rows 70 / 65 (the slower one is
+// taken), 6 rows 82 / 71; one of 4096 x 4096, 8 rows 13.1 / 16.6, 16 rows 18.0 / 16.7 (hence G + 1).
+// What the count costs where rows are unlike routed ones: 32 groups of 2048 x 7168 with one row
+// each, but 100 / 123 in one of them, 182 / 195 against 173 / 173; all 64 / 154 rows in one of the
+// groups, 53 / 92 against 27 / 48; 8 groups of 14336 x 4096 with 4 rows each in a buffer of 4096
+// rows, 180 (tiles of 192 tokens are taken) against 128.
 static cudaError_t launch_w4_product(int act, const void* a, int64_t a_rows, int K,
                                      const moe_w4_t* gate, const moe_w4_t* w, int G, int N,
                                      const int32_t* offsets, void* out, cudaStream_t s) {

@@ -15,9 +15,10 @@
 // Both only stream memory (a few operations a byte).  The merge's gradient keeps a token's dout
 // in registers (4 vectors of 16 bytes a lane, as many warps a token as its row needs) and reads
 // it once for all of the token's experts: the bytes are dout + y + dy.  4096 tokens top-2 of D =
-// 4096, bf16: 29.6 us, 88% of the copy rate (33 with two rows of y under way at a time, 40 with 2
-// vectors a lane); 8190 tokens under expert choice, 64 x 256 rows of D = 2048: 35.5 us, 77% (41 and
-// 48).  The dispatch's gradient, 4096 tokens top-8 of D = 7168: 81 us (100 with 2 vectors a lane).
+// 4096, bf16: 29.7 us, 88% of the copy rate (33 with two rows of y under way at a time, 40 with 2
+// vectors a lane, 29.7 with 8); 8190 tokens under expert choice, 64 x 256 rows of D = 2048: 35.2 us,
+// 77% (41, 48 and 37).  The dispatch's gradient, 4096 tokens top-8 of D = 7168, a quarter of the rows
+// dropped: 81 us, 90% (98 with 2 vectors a lane, 205 with 8).
 #include "common.cuh"
 
 namespace moe {

@@ -24,9 +24,6 @@ namespace moe {
 
 constexpr int W4_BLOCK = 64;                    // k per block of the code layout (32 bytes)
 
-// First k, within its block, of word w (0..7).
-__host__ __device__ __forceinline__ int w4_word_k(int w) { return 32 * (w & 1) + 8 * (w >> 1); }
-
 __device__ __forceinline__ float w4_scale(uint8_t s) {
   __nv_fp8_e4m3 v;
   v.__x = s;

@@ -13,8 +13,8 @@
 // whose largest t is below 2^-100 counts as zeros (row_scale 0), so 1 / step is always finite.
 //
 // Both directions stream memory: the wide weights once, the 4-bit form once (8 x 14336 x 4096 with
-// groups of 128, at the measured copy rate 183 us for bf16, 328 for fp32: quantise 235 and 334 us,
-// dequantise 197 and 349).  For bf16 the instructions cost more than that (schedulers 84% busy),
+// groups of 128, at the measured copy rate 183 us for bf16, 328 for fp32: quantise 235 and 337 us,
+// dequantise 200 and 349, each alone; quantise, then dequantise, bf16, 460).  For bf16 the instructions cost more than that (schedulers 84% busy),
 // which shapes both kernels: rounding by adding 1.5 * 2^23 and packing by multiply-add on the sums'
 // bits instead of conversion instructions, a group's three divisions by one lane for the whole
 // group, scales through shared memory (they are stored [group, row]: a row's own are N bytes

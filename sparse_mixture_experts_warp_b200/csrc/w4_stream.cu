@@ -12,7 +12,8 @@
 //     k instead of one per weight);
 //   - the product runs in fp16, whose 10 mantissa bits take a nibble at bits 0..3 or 4..7 of a
 //     half word: one shift and four mask-and-or steps per 8 codes (bf16's 7 bits need three
-//     shifts).  A token row is scaled by the power of two that brings its largest element to
+//     shifts; putting a nibble into the mantissa of 1024 and taking 1024 off again is the method of
+//     Kim et al., "Who Says Elephants Can't Run", 2022).  A token row is scaled by the power of two that brings its largest element to
 //     [2^14, 2^15): its bf16 elements are then fp16 numbers exactly down to 2^-32 of the largest,
 //     and what lies below is off by at most 2^-39 of it, far under the fp32 sums' own rounding.
 //     The inverse power multiplies the finished sum.
